@@ -19,11 +19,18 @@ The functions carry the C entry points' names:
   device array of ``ATTN_NOALLOC_SCRATCH_BYTES``)
 * ``attn_fwd_merge``, ``attn_merge_partial``, ``attn_accumulate``: the folds of ring
   attention's partial results (``exact_io_aware_46_b200.ring`` drives them)
+* ``attn_fwd_diff(Q, K, V, lam, ...) -> (O, O2, LSE)``: differential attention (two softmax
+  maps a head, subtracted with a learned weight)
+* ``attn_fwd_splitkv_decode_diff`` / ``attn_fwd_splitkv_decode_diff_paged(...) -> (O, LSE)``: the
+  same for one new token per sequence over a cache
+* ``attn_kv_append_paged(K, V, Kpages, Vpages, block_table, k_lens, ...)``: new tokens' keys and
+  values into a paged cache, with the position rotation applied on the way
 * the ``*_workspace_size`` queries and the device-status helpers.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -48,6 +55,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _f = ctypes.c_float
+_ll = ctypes.c_longlong
 
 #: exported symbol -> (restype, argtypes); mirrors include/attn.h
 SIGNATURES = {
@@ -79,6 +87,18 @@ SIGNATURES = {
                                              _vp, _vp]),
     "attn_fwd_splitkv_decode_paged": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i,
                                            _i, _f, _vp, _vp, _sz, _vp]),
+    "attn_fwd_diff_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "attn_fwd_diff": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i,
+                           _vp, _vp, _sz, _vp]),
+    "attn_decode_diff_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "attn_fwd_splitkv_decode_diff": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
+                                          _f, _vp, _vp, _sz, _vp]),
+    "attn_fwd_splitkv_decode_diff_paged": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp,
+                                                _i, _i, _i, _i, _f, _vp, _vp, _sz, _vp]),
+    "attn_kv_append_paged_workspace_size": (_sz, []),
+    "attn_kv_append_paged": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i,
+                                  _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _sz,
+                                  _vp]),
     "attn_read_device_status": (_i, [_vp, _vp, ctypes.POINTER(ctypes.c_int32)]),
     "attn_clear_device_status": (_i, [_vp, _vp]),
 }
@@ -564,3 +584,249 @@ def attn_bwd(Q, K, V, O, dO, lse, scale=None, causal=False, k_lens=None, dQ=None
                           _stream(stream))
     _check(code, "attn_bwd")
     return dQ, dK, dV
+
+
+# ------------------------------------------------------------------ differential attention
+
+
+@contextlib.contextmanager
+def _launch_on(dev, stream):
+    """Runs a call on ``stream`` (default: the current stream of the tensors' device): what it
+    allocates belongs to that stream, and the tensors' device is current meanwhile.  Yields
+    the stream's handle."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+    else:
+        with torch.cuda.device(dev):
+            yield torch.cuda.current_stream(dev).cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _new_workspace(nbytes, dev, handle):
+    ws = torch.empty(max(256, int(nbytes)), dtype=torch.uint8, device=dev)
+    _check(lib().attn_clear_device_status(ws.data_ptr(), handle), "attn_clear_device_status")
+    return ws
+
+
+def _lam(lam, Hq, dev):
+    _need(lam, "lam", torch.float32, device=dev)
+    if lam.dim() != 1 or lam.numel() not in (1, Hq):
+        raise ValueError(f"lam must be [{Hq}] or [1], got {tuple(lam.shape)}")
+    return int(lam.numel())
+
+
+def attn_fwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d) -> int:
+    return int(lib().attn_fwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d))
+
+
+def attn_decode_diff_workspace_size(B, Hq, Hkv, Lmax, d) -> int:
+    return int(lib().attn_decode_diff_workspace_size(B, Hq, Hkv, Lmax, d))
+
+
+def attn_fwd_diff(Q, K, V, lam, scale=None, causal=False, k_lens=None, O=None, O2=None, lse=None,
+                  workspace=None, stream=None, want_aux=True):
+    """Differential attention: each head row holds two maps' halves, Q = [q1 q2] and
+    K = [k1 k2], and O = softmax(scale q1 k1^T) V - lam softmax(scale q2 k2^T) V.
+
+    Q [B,Hq,Lq,d], K/V [B,Hkv,Lk,d] bf16; lam fp32 [Hq] or [1]; scale defaults to
+    1/sqrt(d / 2).  Returns (O, O2, LSE): O2 [B,Hq,Lq,d] bf16, the second map's output, and
+    LSE fp32 [B,Hq,2,Lq] are what attn_bwd_diff needs (None if ``want_aux`` is False and they
+    are not passed in)."""
+    B, Hq, Hkv, Lq, Lk, d, dev = _qkv(Q, K, V)
+    n_lam = _lam(lam, Hq, dev)
+    _klens(k_lens, B, dev)
+    _opt(O, "O", torch.bfloat16, (B, Hq, Lq, d), dev)
+    _opt(O2, "O2", torch.bfloat16, (B, Hq, Lq, d), dev)
+    _opt(lse, "lse", torch.float32, (B, Hq, 2, Lq), dev)
+    nbytes = attn_fwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d)
+    if workspace is not None:
+        _ws_check(workspace, nbytes, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d / 2)
+    with _launch_on(dev, stream) as handle:
+        if workspace is None:
+            workspace = _new_workspace(nbytes, dev, handle)
+        if O is None:
+            O = torch.empty_like(Q)
+        if want_aux:
+            O2 = torch.empty_like(Q) if O2 is None else O2
+            if lse is None:
+                lse = torch.empty((B, Hq, 2, Lq), dtype=torch.float32, device=dev)
+        code = lib().attn_fwd_diff(_addr(Q), _addr(K), _addr(V), _addr(lam), n_lam, _addr(O),
+                                   _addr(O2), _addr(lse), B, Hq, Hkv, Lq, Lk, d, float(scale),
+                                   _mask(causal), _addr(k_lens), _addr(workspace),
+                                   workspace.numel(), handle)
+    _check(code, "attn_fwd_diff")
+    return O, O2, lse
+
+
+def _decode_diff(Q, Kc, Vc, block_table, lam, k_lens, scale, O, lse, workspace, stream, want_lse):
+    """Both differential decodes: contiguous cache (``block_table`` None) or pages."""
+    paged = block_table is not None
+    names = ("Kpages", "Vpages") if paged else ("Kcache", "Vcache")
+    B, Hq, Hkv, d, dev = _decode_args(Q, Kc, Vc, k_lens, O, None, names)
+    n_lam = _lam(lam, Hq, dev)
+    _opt(lse, "lse", torch.float32, (B, Hq, 2), dev)
+    rows = int(Kc.shape[2])
+    if paged:
+        _need(block_table, "block_table", torch.int32, device=dev)
+        if block_table.dim() != 2 or int(block_table.shape[0]) != B:
+            raise ValueError(f"block_table must be [{B}, max_blocks], "
+                             f"got {tuple(block_table.shape)}")
+        max_blocks = int(block_table.shape[1])
+        Lmax = max_blocks * rows
+    else:
+        if int(Kc.shape[0]) != B:
+            raise ValueError(f"Kcache must be [{B}, Hkv, Lmax, {d}], got {tuple(Kc.shape)}")
+        Lmax = rows
+    if Lmax > 1 << 30:
+        raise ValueError(f"a cache of {Lmax} rows a sequence is past the limit of 2^30")
+    nbytes = attn_decode_diff_workspace_size(B, Hq, Hkv, Lmax, d)
+    if workspace is not None:
+        _ws_check(workspace, nbytes, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d / 2)
+    with _launch_on(dev, stream) as handle:
+        if workspace is None:
+            workspace = _new_workspace(nbytes, dev, handle)
+        if O is None:
+            O = torch.empty_like(Q)
+        if lse is None and want_lse:
+            lse = torch.empty((B, Hq, 2), dtype=torch.float32, device=dev)
+        tail = (d, float(scale), _addr(k_lens), _addr(workspace), workspace.numel(), handle)
+        if paged:
+            name = "attn_fwd_splitkv_decode_diff_paged"
+            code = lib().attn_fwd_splitkv_decode_diff_paged(
+                _addr(Q), _addr(Kc), _addr(Vc), _addr(block_table), max_blocks, rows,
+                int(Kc.shape[0]), _addr(lam), n_lam, _addr(O), _addr(lse), B, Hq, Hkv, *tail)
+        else:
+            name = "attn_fwd_splitkv_decode_diff"
+            code = lib().attn_fwd_splitkv_decode_diff(
+                _addr(Q), _addr(Kc), _addr(Vc), _addr(lam), n_lam, _addr(O), _addr(lse), B, Hq,
+                Hkv, Lmax, *tail)
+    _check(code, name)
+    return O, lse
+
+
+def attn_fwd_splitkv_decode_diff(Q, Kc, Vc, lam, k_lens, scale=None, O=None, lse=None,
+                                 workspace=None, stream=None, want_lse=True):
+    """attn_fwd_diff of one new token per sequence over a cache.  Q [B,Hq,1,d]; Kc/Vc
+    [B,Hkv,Lmax,d] bf16; lam fp32 [Hq] or [1]; k_lens int32 [B].  Returns (O [B,Hq,1,d] bf16,
+    LSE [B,Hq,2] fp32)."""
+    return _decode_diff(Q, Kc, Vc, None, lam, k_lens, scale, O, lse, workspace, stream, want_lse)
+
+
+def attn_fwd_splitkv_decode_diff_paged(Q, Kp, Vp, block_table, lam, k_lens, scale=None, O=None,
+                                       lse=None, workspace=None, stream=None, want_lse=True):
+    """The same over a paged cache: Kp/Vp [n_pages,Hkv,page,d] bf16; block_table int32
+    [B,max_blocks]."""
+    if block_table is None:
+        raise ValueError("block_table is required")
+    return _decode_diff(Q, Kp, Vp, block_table, lam, k_lens, scale, O, lse, workspace, stream,
+                        want_lse)
+
+
+# ------------------------------------------------------------------ append to a paged cache
+
+
+def attn_kv_append_paged_workspace_size() -> int:
+    return int(lib().attn_kv_append_paged_workspace_size())
+
+
+def _tokens(t, name, d, dev, heads=None, T=None):
+    """New tokens [T, H, d] bf16 whose head rows are contiguous within a token (any token
+    stride that is a multiple of 8: views of a fused projection).  Returns (T, H, stride)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name} must be a CUDA tensor (host memory is not accepted; "
+                         f"there is no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.dim() != 3 or int(t.shape[2]) != d or (heads is not None and int(t.shape[1]) != heads) \
+            or (T is not None and int(t.shape[0]) != T):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"[{'T' if T is None else T}, {'H' if heads is None else heads}, {d}]")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    T, H = int(t.shape[0]), int(t.shape[1])
+    stride = H * d
+    if not t.is_contiguous():
+        s0, s1, s2 = (int(x) for x in t.stride())
+        if s2 != 1 or (H > 1 and s1 != d) or (T > 1 and (s0 % 8 != 0 or s0 < H * d)):
+            raise ValueError(f"{name} has strides {(s0, s1, s2)}: a token's rows must be "
+                             f"contiguous, its tokens a multiple of 8 elements apart")
+        stride = s0 if T > 1 else H * d
+    return T, H, stride
+
+
+def attn_kv_append_paged(K, V, Kp, Vp, block_table, k_lens, cu_seqlens=None, Q=None, Q_out=None,
+                         cos=None, sin=None, maps=1, interleaved=False, workspace=None,
+                         stream=None):
+    """Appends new tokens to a paged cache, rotating K (and Q) by position on the way.
+
+    K/V [T,Hkv,d] and Q [T,Hq,d] bf16, packed; tokens may be strided (views of a fused
+    projection).  Kp/Vp [n_pages,Hkv,page,d]; block_table int32 [B,max_blocks]; k_lens int32 [B],
+    the lengths AFTER the append (those of the decode that follows); cu_seqlens int32 [B+1]
+    gives each sequence's new tokens (None: one token per sequence).  cos/sin fp32
+    [n_pos, rope_dim/2] or both None (no rotation); maps = 2 rotates each half of a
+    differential head by itself.  Returns the rotated Q [T,Hq,d] (None without Q); rows behind
+    the last sequence are left as they were."""
+    _need(Kp, "Kpages", torch.bfloat16)
+    if Kp.dim() != 4:
+        raise ValueError(f"Kpages must be [n_pages, Hkv, page, d], got {tuple(Kp.shape)}")
+    n_pages, Hkv, page, d = (int(x) for x in Kp.shape)
+    dev = Kp.device
+    _need(Vp, "Vpages", torch.bfloat16, (n_pages, Hkv, page, d), dev)
+    T, _, ks = _tokens(K, "K", d, dev, Hkv)
+    _, _, vs = _tokens(V, "V", d, dev, Hkv, T)
+    _need(k_lens, "k_lens", torch.int32, device=dev)
+    if k_lens.dim() != 1 or k_lens.numel() < 1:
+        raise ValueError("k_lens must be a 1-D int32 tensor of B lengths")
+    B = int(k_lens.numel())
+    if cu_seqlens is None:
+        if T != B:
+            raise ValueError(f"{T} tokens for {B} sequences: pass cu_seqlens unless every "
+                             f"sequence has one new token")
+    else:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    _need(block_table, "block_table", torch.int32, device=dev)
+    if block_table.dim() != 2 or int(block_table.shape[0]) != B:
+        raise ValueError(f"block_table must be [{B}, max_blocks], got {tuple(block_table.shape)}")
+    Hq, qs = Hkv, 0
+    if Q is not None:
+        _, Hq, qs = _tokens(Q, "Q", d, dev, None, T)
+        _heads(Hq, Hkv)
+        _opt(Q_out, "Q_out", torch.bfloat16, (T, Hq, d), dev)
+    elif Q_out is not None:
+        raise ValueError("Q_out without Q")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    n_pos = rope = 0
+    if cos is not None:
+        _need(cos, "cos", torch.float32, device=dev)
+        if cos.dim() != 2:
+            raise ValueError(f"cos must be [n_pos, rope_dim / 2], got {tuple(cos.shape)}")
+        n_pos, rope = int(cos.shape[0]), 2 * int(cos.shape[1])
+        _need(sin, "sin", torch.float32, tuple(cos.shape), dev)
+    nbytes = attn_kv_append_paged_workspace_size()
+    if workspace is not None:
+        _ws_check(workspace, nbytes, dev)
+    with _launch_on(dev, stream) as handle:
+        if workspace is None:
+            workspace = _new_workspace(nbytes, dev, handle)
+        if Q is not None and Q_out is None:
+            Q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        code = lib().attn_kv_append_paged(
+            _addr(Q), qs, _addr(K), ks, _addr(V), vs, _addr(Q_out), _addr(Kp), _addr(Vp),
+            _addr(block_table), int(block_table.shape[1]), page, n_pages, _addr(cu_seqlens),
+            _addr(k_lens), B, T, Hq, Hkv, d, _addr(cos), _addr(sin), n_pos, rope, int(maps),
+            1 if interleaved else 0, _addr(workspace), workspace.numel(), handle)
+    _check(code, "attn_kv_append_paged")
+    return Q_out

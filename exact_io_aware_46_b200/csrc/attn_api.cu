@@ -12,6 +12,7 @@
 
 #include "../../include/attn.h"
 #include "accum_kernel.cuh"
+#include "append_kernel.cuh"
 #include "bwd_kernel.cuh"
 #include "decode_kernel.cuh"
 #include "fwd_kernel.cuh"
@@ -23,6 +24,7 @@ namespace {
 constexpr size_t kStatusBytes = 256;  // status word + scheduler counters, 256-byte aligned
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -109,6 +111,12 @@ bool shapes_ok(int B, int Hq, int Hkv, int Lq, int Lk) {
   return true;
 }
 
+// The differential kernels count their work items (128-row tiles of every head) and
+// the rows of a tile's head in 32 bits.
+bool items_ok(int B, int H, int L) {
+  return static_cast<long long>(B) * H * ((L + 127LL) / 128) <= (1LL << 30);
+}
+
 using attn_host::set_smem;
 
 }  // namespace
@@ -156,7 +164,9 @@ static attn_status_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, co
   const int sms = device_sms();
   if (sms <= 0) return ATTN_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int n_pairs = (p.Lq + 2 * attn_fwd_impl::BM - 1) / (2 * attn_fwd_impl::BM);
+  // rows of an item: a pair of query tiles, or one tile of a differential head's two maps
+  const int item_rows = (p.lam ? 1 : 2) * attn_fwd_impl::BM;
+  const int n_pairs = (p.Lq + item_rows - 1) / item_rows;
   const int n_items = B * Hq * n_pairs;
   p.O = reinterpret_cast<__nv_bfloat16*>(O);
   p.lse = lse;
@@ -170,7 +180,8 @@ static attn_status_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, co
   p.n_pairs = n_pairs;
   p.n_items = n_items;
   const int grid = n_items < sms ? n_items : sms;
-  const int mode = p.cu_q      ? attn_fwd_impl::MODE_VARLEN
+  const int mode = p.lam       ? attn_fwd_impl::MODE_DIFF
+                   : p.cu_q    ? attn_fwd_impl::MODE_VARLEN
                    : p.q_scale ? attn_fwd_impl::MODE_FP8
                    : p.o_acc   ? attn_fwd_impl::MODE_MERGE
                    : p.window > 0 ? attn_fwd_impl::MODE_WINDOW
@@ -187,6 +198,7 @@ static attn_status_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, co
     else if (mode == MODE_WINDOW) run(fwd_kernel<128, MODE_WINDOW>, smem);
     else if (mode == MODE_FP8) run(fwd_kernel<128, MODE_FP8>, Cfg<128, 1>::SMEM_BYTES);
     else if (mode == MODE_MERGE) run(fwd_kernel<128, MODE_MERGE>, smem);
+    else if (mode == MODE_DIFF) run(fwd_kernel<128, MODE_DIFF>, smem);
     else run(fwd_kernel<128, MODE_VARLEN>, smem);
   } else {
     if (mode == MODE_FP8) return ATTN_ERR_UNSUPPORTED;
@@ -194,6 +206,7 @@ static attn_status_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, co
     if (mode == MODE_PLAIN) run(fwd_kernel<64, MODE_PLAIN>, smem);
     else if (mode == MODE_WINDOW) run(fwd_kernel<64, MODE_WINDOW>, smem);
     else if (mode == MODE_MERGE) run(fwd_kernel<64, MODE_MERGE>, smem);
+    else if (mode == MODE_DIFF) run(fwd_kernel<64, MODE_DIFF>, smem);
     else run(fwd_kernel<64, MODE_VARLEN>, smem);
   }
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
@@ -370,6 +383,45 @@ attn_status_t attn_fwd_varlen(const attn_bf16_t* Q, const attn_bf16_t* K, const 
   return launch_fwd(tq, tk, tv, p, O, lse, B, Hq, Hkv, d, scale, mask_flags, workspace, stream);
 }
 
+// ------------------------------------------------------------------ differential forward
+
+size_t attn_fwd_diff_workspace_size(int, int, int, int, int, int) { return kStatusBytes; }
+
+attn_status_t attn_fwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const attn_bf16_t* V,
+                            const float* lam, int n_lam, attn_bf16_t* O, attn_bf16_t* O2,
+                            float* lse, int B, int Hq, int Hkv, int Lq, int Lk, int d,
+                            float scale, int mask_flags, const int32_t* k_lens, void* workspace,
+                            size_t ws_bytes, void* stream) {
+  if (!shapes_ok(B, Hq, Hkv, Lq, Lk)) return ATTN_ERR_INVALID;
+  if ((Lq > 0 && (!Q || !O)) || (Lk > 0 && (!K || !V)) || !lam || !workspace)
+    return ATTN_ERR_INVALID;
+  if (n_lam != 1 && n_lam != Hq) return ATTN_ERR_INVALID;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned4(lam) ||
+      (O2 && !aligned16(O2)) || (lse && !aligned16(lse)) || (k_lens && !aligned16(k_lens)) ||
+      !aligned256(workspace))
+    return ATTN_ERR_INVALID;
+  if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_INVALID;
+  if (mask_flags != ATTN_MASK_NONE && mask_flags != ATTN_MASK_CAUSAL) return ATTN_ERR_INVALID;
+  if (ws_bytes < attn_fwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d)) return ATTN_ERR_INVALID;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!items_ok(B, Hq, Lq) || !items_ok(B, Hkv, Lk)) return ATTN_ERR_UNSUPPORTED;
+  if (Lq == 0) return ATTN_OK;
+  if (Lk == 0) K = V = Q;  // no tile is loaded; the maps only need an address
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap(&tq, Q, d, Lq, static_cast<long long>(B) * Hq, 128) ||
+      !make_tmap(&tk, K, d, Lk, static_cast<long long>(B) * Hkv, 128) ||
+      !make_tmap(&tv, V, d, Lk, static_cast<long long>(B) * Hkv, 128))
+    return ATTN_ERR_CUDA;
+  attn_fwd_impl::Params p{};
+  p.k_lens = k_lens;
+  p.Lq = Lq;
+  p.Lk = Lk;
+  p.lam = lam;
+  p.n_lam = n_lam;
+  p.O2 = reinterpret_cast<__nv_bfloat16*>(O2);
+  return launch_fwd(tq, tk, tv, p, O, lse, B, Hq, Hkv, d, scale, mask_flags, workspace, stream);
+}
+
 // ------------------------------------------------------------------ merge of partials
 
 attn_status_t attn_merge_partial(const attn_bf16_t* O_part, const float* lse_part, float* O_acc,
@@ -492,6 +544,152 @@ attn_status_t attn_fwd_splitkv_decode_paged(const attn_bf16_t* Q, const attn_bf1
       Hkv, Lmax, d, scale, k_lens, reinterpret_cast<int*>(workspace),
       reinterpret_cast<uint8_t*>(workspace) + kStatusBytes, sms, s, &pg);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ differential decode
+
+size_t attn_decode_diff_workspace_size(int B, int Hq, int Hkv, int Lmax, int d) {
+  if (!shapes_ok(B, Hq, Hkv, 1, Lmax) || d < 0) return kStatusBytes;
+  return kStatusBytes + attn_decode_impl::diff_partials_bytes(B, Hq, Hkv, Lmax, d);
+}
+
+// Checks and launch shared by the contiguous (page_size = 0) and the paged entry point.
+static attn_status_t decode_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const attn_bf16_t* V,
+                                 const int32_t* block_table, int max_blocks, int page_size,
+                                 int n_pages, const float* lam, int n_lam, attn_bf16_t* O,
+                                 float* lse, int B, int Hq, int Hkv, int Lmax, int d, float scale,
+                                 const int32_t* k_lens, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  if (!shapes_ok(B, Hq, Hkv, 1, Lmax)) return ATTN_ERR_INVALID;
+  if (!Q || (Lmax > 0 && (!K || !V)) || !lam || !O || !k_lens || !workspace ||
+      (page_size && !block_table))
+    return ATTN_ERR_INVALID;
+  if (n_lam != 1 && n_lam != Hq) return ATTN_ERR_INVALID;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned4(lam) ||
+      (lse && !aligned16(lse)) || !aligned16(k_lens) || (page_size && !aligned16(block_table)) ||
+      !aligned256(workspace))
+    return ATTN_ERR_INVALID;
+  if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_INVALID;
+  if (ws_bytes < attn_decode_diff_workspace_size(B, Hq, Hkv, Lmax, d)) return ATTN_ERR_INVALID;
+  if (d != 128 && d != 64) return ATTN_ERR_UNSUPPORTED;
+  // a group's heads take two of the 16 columns of the score product each
+  if (Hq / Hkv > 8) return ATTN_ERR_UNSUPPORTED;
+  if (!attn_decode_impl::supported_shape(B, Hkv, Lmax, page_size)) return ATTN_ERR_UNSUPPORTED;
+  if (Lmax == 0) K = V = Q;  // nothing is loaded; the maps only need an address
+  int page_log2 = 0;
+  while ((1 << page_log2) < page_size) ++page_log2;
+  const attn_decode_impl::PagedKV pg{block_table, max_blocks, page_log2, n_pages};
+  const cudaError_t e = attn_decode_impl::launch_diff(
+      reinterpret_cast<const __nv_bfloat16*>(Q), reinterpret_cast<const __nv_bfloat16*>(K),
+      reinterpret_cast<const __nv_bfloat16*>(V), lam, n_lam, reinterpret_cast<__nv_bfloat16*>(O),
+      lse, B, Hq, Hkv, Lmax, d, scale, k_lens, reinterpret_cast<int*>(workspace),
+      reinterpret_cast<uint8_t*>(workspace) + kStatusBytes,
+      reinterpret_cast<cudaStream_t>(stream), page_size ? &pg : nullptr);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_fwd_splitkv_decode_diff(const attn_bf16_t* Q, const attn_bf16_t* Kc,
+                                           const attn_bf16_t* Vc, const float* lam, int n_lam,
+                                           attn_bf16_t* O, float* lse, int B, int Hq, int Hkv,
+                                           int Lmax, int d, float scale, const int32_t* k_lens,
+                                           void* workspace, size_t ws_bytes, void* stream) {
+  return decode_diff(Q, Kc, Vc, nullptr, 0, 0, 0, lam, n_lam, O, lse, B, Hq, Hkv, Lmax, d, scale,
+                     k_lens, workspace, ws_bytes, stream);
+}
+
+// Rows a block table can address, or an error: the page sizes and the limit of the paged decode.
+static attn_status_t paged_capacity(int max_blocks, int page_size, int n_pages, int* Lmax) {
+  if (max_blocks <= 0 || n_pages <= 0 || page_size <= 0) return ATTN_ERR_INVALID;
+  if ((page_size & (page_size - 1)) != 0 || page_size < 16 || page_size > 65536)
+    return ATTN_ERR_UNSUPPORTED;
+  const long long lmax = static_cast<long long>(max_blocks) * page_size;
+  if (lmax > (1 << 30)) return ATTN_ERR_INVALID;
+  *Lmax = static_cast<int>(lmax);
+  return ATTN_OK;
+}
+
+attn_status_t attn_fwd_splitkv_decode_diff_paged(
+    const attn_bf16_t* Q, const attn_bf16_t* Kp, const attn_bf16_t* Vp,
+    const int32_t* block_table, int max_blocks, int page_size, int n_pages, const float* lam,
+    int n_lam, attn_bf16_t* O, float* lse, int B, int Hq, int Hkv, int d, float scale,
+    const int32_t* k_lens, void* workspace, size_t ws_bytes, void* stream) {
+  int Lmax = 0;
+  const attn_status_t st = paged_capacity(max_blocks, page_size, n_pages, &Lmax);
+  if (st != ATTN_OK) return st;
+  return decode_diff(Q, Kp, Vp, block_table, max_blocks, page_size, n_pages, lam, n_lam, O, lse,
+                     B, Hq, Hkv, Lmax, d, scale, k_lens, workspace, ws_bytes, stream);
+}
+
+// ------------------------------------------------------------------ append to a paged cache
+
+size_t attn_kv_append_paged_workspace_size(void) { return kStatusBytes; }
+
+attn_status_t attn_kv_append_paged(const attn_bf16_t* Q, long long q_stride, const attn_bf16_t* K,
+                                   long long k_stride, const attn_bf16_t* V, long long v_stride,
+                                   attn_bf16_t* Q_out, attn_bf16_t* Kp, attn_bf16_t* Vp,
+                                   const int32_t* block_table, int max_blocks, int page_size,
+                                   int n_pages, const int32_t* cu_seqlens, const int32_t* k_lens,
+                                   int B, int T, int Hq, int Hkv, int d, const float* cos_table,
+                                   const float* sin_table, int n_pos, int rope_dim, int maps,
+                                   int interleaved, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  int Lmax = 0;
+  const attn_status_t st = paged_capacity(max_blocks, page_size, n_pages, &Lmax);
+  if (st != ATTN_OK) return st;
+  if (!shapes_ok(B, Hq, Hkv, T, Lmax)) return ATTN_ERR_INVALID;
+  if ((T > 0 && (!K || !V)) || !Kp || !Vp || !block_table || !k_lens || !workspace)
+    return ATTN_ERR_INVALID;
+  if ((Q == nullptr) != (Q_out == nullptr)) return ATTN_ERR_INVALID;
+  if (!cu_seqlens && T != B) return ATTN_ERR_INVALID;  // one token per sequence
+  if ((maps != 1 && maps != 2) || (interleaved != 0 && interleaved != 1) || rope_dim < 0 ||
+      n_pos < 0)
+    return ATTN_ERR_INVALID;
+  if (rope_dim > 0 && (!cos_table || !sin_table || n_pos < 1)) return ATTN_ERR_INVALID;
+  const void* p16[] = {Q, K, V, Q_out, Kp, Vp, block_table, cu_seqlens, k_lens, cos_table,
+                       sin_table};
+  for (const void* q : p16)
+    if (!aligned16(q)) return ATTN_ERR_INVALID;  // a null pointer passes
+  if (!aligned256(workspace)) return ATTN_ERR_INVALID;
+  const long long qs = Q ? q_stride : 0;
+  if ((qs & 7) || (k_stride & 7) || (v_stride & 7) || (Q && qs < 0) || k_stride < 0 ||
+      v_stride < 0)
+    return ATTN_ERR_INVALID;
+  if (ws_bytes < kStatusBytes) return ATTN_ERR_INVALID;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (rope_dim % 16 != 0 || rope_dim > d / maps) return ATTN_ERR_UNSUPPORTED;
+  if (T == 0) return ATTN_OK;
+  const int sms = device_sms();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  attn_append_impl::Params p{};
+  p.Q = reinterpret_cast<const __nv_bfloat16*>(Q);
+  p.K = reinterpret_cast<const __nv_bfloat16*>(K);
+  p.V = reinterpret_cast<const __nv_bfloat16*>(V);
+  p.q_stride = qs;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.Q_out = reinterpret_cast<__nv_bfloat16*>(Q_out);
+  p.Kp = reinterpret_cast<__nv_bfloat16*>(Kp);
+  p.Vp = reinterpret_cast<__nv_bfloat16*>(Vp);
+  p.block_table = block_table;
+  p.cu = cu_seqlens;
+  p.k_lens = k_lens;
+  p.cos_t = cos_table;
+  p.sin_t = sin_table;
+  p.status = reinterpret_cast<int*>(workspace);
+  p.B = B;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.max_blocks = max_blocks;
+  while ((1 << p.page_log2) < page_size) ++p.page_log2;
+  p.n_pages = n_pages;
+  p.n_pos = n_pos;
+  p.rope = rope_dim;
+  p.maps = maps;
+  p.interleaved = interleaved;
+  p.q_rows = Q ? Hq : 0;
+  const cudaError_t e = attn_append_impl::launch(p, d, sms, reinterpret_cast<cudaStream_t>(stream));
+  return attn_host::report(e, "append_kernel") == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ backward

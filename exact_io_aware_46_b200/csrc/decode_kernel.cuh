@@ -61,6 +61,7 @@ struct SplitParams {
   // row r of sequence b lives in page block_table[b * max_blocks + r / page]
   const int* block_table;
   int max_blocks, page_log2, n_pages;
+  int ch;  // keys per split of the differential decode (the plain one: CH)
 };
 
 // The grid is (sequence x kv head, chunk position counted from the sequence's
@@ -104,6 +105,16 @@ __device__ __forceinline__ int valid_klen(const int* k_lens, int b, int Lmax, in
 // threshold and write the chunk's normalised partial.  The block chain (S, softmax, PV) is serial;
 // with two CTAs per SM and the next block's K and V in flight during it, the
 // copies are the limit.
+//
+// Differential heads (DIFF): a head row holds the halves of two maps, [q1 q2] and
+// [k1 k2], whose softmaxes share V.  Head g's two maps are two of the 16 columns,
+// 2g with [q1 0] and 2g + 1 with [0 q2] as their Q rows, so the same two MMAs
+// give both maps' scores and both O^T over one read of K and V; the combine
+// subtracts.  Measured on B200 (B64 Hq32 Hkv8 d128, k_len ~ U[1024, 32768],
+// 64-row pages): see diff_chunk below.  Keys past the sequence's end may hold
+// anything (a page is handed out unwritten): their scores are dropped by
+// selection, and their V rows, which a zero probability would not silence if
+// they held NaN, are cleared in shared memory before the PV product.
 namespace tc {
 
 // 4-D tiled copy global -> shared; completion counted on `bar` in bytes.
@@ -138,7 +149,7 @@ constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 // a 128-key block is copied as page segments of min(page, 128) rows (4-D tensor
 // map), and segments past the sequence's last page are addressed at page
 // n_pages, out of range, so the copy fills them with zeros.
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool DIFF = false>
 __global__ void __launch_bounds__(NTHREADS, 2)
     split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const SplitParams p) {
@@ -169,10 +180,16 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   const int hkv = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
   const int kl = valid_klen(p.k_lens, b, p.Lmax, p.status,
                             blockIdx.y == gridDim.y - 1 && hkv == 0 && threadIdx.x == 0);
-  const int chunk = (kl + CH - 1) / CH - static_cast<int>(gridDim.y - blockIdx.y);
+  const int ch = DIFF ? p.ch : CH;
+  const int chunk = (kl + ch - 1) / ch - static_cast<int>(gridDim.y - blockIdx.y);
   if (chunk < 0) return;
-  const int k0 = chunk * CH;
-  const int rows = min(CH, kl - k0);
+  const int k0 = chunk * ch;
+  const int rows = min(ch, kl - k0);
+  // columns in use, and the slot of column h's partial among the sequence's chunks
+  const int ncol = DIFF ? 2 * p.G : p.G;
+  auto part_slot = [&](int h) -> size_t {
+    return (static_cast<size_t>(b) * p.Hq * (DIFF ? 2 : 1) + hkv * ncol + h) * p.nsm + chunk;
+  };
   const int nblk = (rows + BK - 1) / BK;
   const int warp = threadIdx.x >> 5;
   const int head_kv = b * p.Hkv + hkv;
@@ -188,8 +205,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     }
     if (__syncthreads_or(bad_page)) {
       if (threadIdx.x == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
-      for (int e = threadIdx.x; e < p.G * D; e += NTHREADS) {
-        const size_t ph = (static_cast<size_t>(b) * p.Hq + hkv * p.G + e / D) * p.nsm + chunk;
+      for (int e = threadIdx.x; e < ncol * D; e += NTHREADS) {
+        const size_t ph = part_slot(e / D);
         p.part_o[ph * D + e % D] = 0.f;
         if (e % D == 0) p.part_lse[ph] = -INFINITY;
       }
@@ -318,15 +335,21 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     for (int e = t; e < NH * (D / 8); e += 128) {
       const int g = e / (D / 8), c16 = e % (D / 8);
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (g < G)
-        v = __ldg(reinterpret_cast<const uint4*>(
-                      p.Q + (static_cast<size_t>(b) * p.Hq + hkv * G + g) * D) + c16);
+      if constexpr (DIFF) {  // column g: map g % 2 of the group's head g / 2
+        if (g < ncol && c16 / (D / 16) == (g & 1))
+          v = __ldg(reinterpret_cast<const uint4*>(
+                        p.Q + (static_cast<size_t>(b) * p.Hq + hkv * G + (g >> 1)) * D) + c16);
+      } else {
+        if (g < G)
+          v = __ldg(reinterpret_cast<const uint4*>(
+                        p.Q + (static_cast<size_t>(b) * p.Hq + hkv * G + g) * D) + c16);
+      }
       *reinterpret_cast<uint4*>(smem + OFF_Q + (c16 >> 3) * HPANEL + g * 128 +
                                 (((c16 & 7) ^ (g & 7)) << 4)) = v;
     }
     for (int e = t; e < NH * 16; e += 128) {
       const int g = e >> 4, c16 = e & 15;
-      if (g >= G)
+      if (g >= ncol)
         *reinterpret_cast<uint4*>(smem + OFF_P + (c16 >> 3) * HPANEL + g * 128 + ((c16 & 7) << 4)) =
             make_uint4(0u, 0u, 0u, 0u);
     }
@@ -360,7 +383,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       float v[NH];
 #pragma unroll
       for (int h = 0; h < NH; ++h)
-        v[h] = (valid && h < G) ? __uint_as_float(s[h]) * p.scale_log2 : -INFINITY;
+        v[h] = (valid && h < ncol) ? __uint_as_float(s[h]) * p.scale_log2 : -INFINITY;
       // block maxima per head: within the warp, then across the four warps
       // (through shared memory and an mbarrier, so that every wait is bounded;
       // two buffers: a warp writes block j + 2's maxima only after all four
@@ -406,11 +429,27 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        if (h < G) {
+        if (h < ncol) {
           const float pv = (v[h] == -INFINITY) ? 0.f : sm100::ex2(v[h] - m_use[h]);
           l[h] += pv;
           *reinterpret_cast<__nv_bfloat16*>(p_col + h * 128 + ((p_chunk ^ (h & 7)) << 4)) =
               __float2bfloat16_rn(pv);
+        }
+      }
+      if constexpr (DIFF) {
+        // the last block's V rows past the sequence's end: zeros (see above)
+        if (j == nblk - 1 && (rows & (BK - 1)) != 0) {  // uniform
+          const int uv = 2 * j + 1, vs = uv % NSLOT;
+          if (!(ok = sm100::mbar_wait(&kv_full[vs], (uv / NSLOT) & 1, abort_flag, p.status, 30)))
+            break;
+          if (!valid) {
+#pragma unroll
+            for (int c = 0; c < DP; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(smem + OFF_RING + vs * SLOT + c * PANEL + r * 128 +
+                                          e * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
       }
       sm100::fence_proxy_async_smem();
@@ -440,9 +479,9 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     const bool live = ok && !*abort_flag;
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      if (h >= G) break;
+      if (h >= ncol) break;
       const float ls = rs[h] + rs[NH + h] + rs[2 * NH + h] + rs[3 * NH + h];
-      const size_t ph = (static_cast<size_t>(b) * p.Hq + hkv * G + h) * p.nsm + chunk;
+      const size_t ph = part_slot(h);
       const bool has = live && ls > 0.f;
       if (r < D) p.part_o[ph * D + r] = has ? __uint_as_float(o[h]) / ls : 0.f;
       if (r == 0) p.part_lse[ph] = has ? m_use[h] + log2f(ls) : -INFINITY;
@@ -491,12 +530,108 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const CombineParams p
     p.lse[bh] = wsum > 0.f ? (M + log2f(wsum)) * 0.69314718055994531f : -INFINITY;
 }
 
+// ---------------------------------------------------------------- differential decode
+
+// Keys per split: the longest of 2048, 1024, 512 and 256 that still gives every
+// SM two chunks of the cache's capacity (the lengths are on the device), since a
+// short grid leaves SMs without a stream of their own.
+inline int diff_chunk(int B, int Hkv, int Lmax) {
+  const long long want = 2 * 148;
+  int ch = CH;
+  while (ch > 256 && static_cast<long long>(B) * Hkv * ((Lmax + ch - 1LL) / ch) < want) ch /= 2;
+  return ch;
+}
+
+inline int diff_splits(int B, int Hkv, int Lmax) {
+  const int ch = diff_chunk(B, Hkv, Lmax);
+  return Lmax > 0 ? (Lmax + ch - 1) / ch : 1;
+}
+
+inline size_t diff_partials_bytes(int B, int Hq, int Hkv, int Lmax, int d) {
+  const size_t n = static_cast<size_t>(B) * Hq * 2 * diff_splits(B, Hkv, Lmax);
+  return (n * d * 4 + n * 4 + 255) & ~static_cast<size_t>(255);
+}
+
+struct DiffCombineParams {
+  const float* part_o;    // [B*Hq][2][nsm][D]
+  const float* part_lse;  // [B*Hq][2][nsm]
+  const int* k_lens;
+  const float* lam;  // [n_lam]
+  __nv_bfloat16* O;
+  float* lse;  // [B*Hq][2] or nullptr
+  int Hq, Lmax, nsm, ch, n_lam;
+};
+
+// Joins both maps' partials (the normalised rule of decode_combine_kernel, per
+// map) and subtracts: O = O_1 - lam O_2.  One block per (sequence, query head),
+// a warp per chunk in turn, each lane D / 32 columns of both maps.
+constexpr int DC_WARPS = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * DC_WARPS) diff_combine_kernel(const DiffCombineParams p) {
+  constexpr int EPL = D / 32;
+  __shared__ float acc_s[DC_WARPS][2][D];
+  const int bh = blockIdx.x, b = bh / p.Hq, h = bh % p.Hq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int kl = __ldg(p.k_lens + b);
+  if (kl < 0 || kl > p.Lmax) kl = 0;  // reported by the split kernel
+  const int n = (kl + p.ch - 1) / p.ch;
+  float M[2], wsum[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const float* lp = p.part_lse + (static_cast<size_t>(bh) * 2 + m) * p.nsm;
+    float x = -INFINITY;
+    for (int c = lane; c < n; c += 32) x = fmaxf(x, lp[c]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    M[m] = x;
+    float ws = 0.f;  // every warp sums all weights: the same value in each
+    for (int c = lane; c < n; c += 32) ws += lp[c] == -INFINITY ? 0.f : sm100::ex2(lp[c] - x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+    wsum[m] = ws;
+    float acc[EPL] = {};
+    const float* op = p.part_o + (static_cast<size_t>(bh) * 2 + m) * p.nsm * D + lane * EPL;
+    for (int c = warp; c < n; c += DC_WARPS) {
+      const float w = lp[c] == -INFINITY ? 0.f : sm100::ex2(lp[c] - x);
+      const float* src = op + static_cast<size_t>(c) * D;
+      if constexpr (EPL == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] += w * v.x; acc[1] += w * v.y; acc[2] += w * v.z; acc[3] += w * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] += w * v.x; acc[1] += w * v.y;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc_s[warp][m][lane * EPL + e] = acc[e];
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float o[2] = {0.f, 0.f};
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+      if (wsum[m] > 0.f) {
+#pragma unroll
+        for (int k = 0; k < DC_WARPS; ++k) o[m] += acc_s[k][m][threadIdx.x];
+        o[m] /= wsum[m];
+      }
+    const float lam = __ldg(p.lam + (p.n_lam == 1 ? 0 : h));
+    p.O[static_cast<size_t>(bh) * D + threadIdx.x] =
+        __float2bfloat16_rn(wsum[0] > 0.f ? o[0] - lam * o[1] : 0.f);
+  }
+  if (p.lse && threadIdx.x < 2) {
+    const float ws = threadIdx.x ? wsum[1] : wsum[0], mx = threadIdx.x ? M[1] : M[0];
+    p.lse[static_cast<size_t>(bh) * 2 + threadIdx.x] =
+        ws > 0.f ? (mx + log2f(ws)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
 // The split kernel and the combine.  Measured on B200
 // (B64 Hq32 Hkv8 d128, cache 32768, k_len ~ U[1024, 32768], 64-row pages in a
 // random order): the paged cache reads at 6951 GB/s, the same rate as the
 // contiguous cache (the earlier CUDA-core split kernel: 6066-6171 GB/s).
-template <int D, bool PAGED>
-cudaError_t launch_tc(const SplitParams& sp, const CombineParams& cp, cudaStream_t s) {
+template <int D, bool PAGED, bool DIFF = false>
+cudaError_t launch_split(const SplitParams& sp, cudaStream_t s) {
   CUtensorMap tk, tv;
   const long long heads = static_cast<long long>(sp.B) * sp.Hkv;
   const int page = 1 << sp.page_log2;
@@ -507,14 +642,19 @@ cudaError_t launch_tc(const SplitParams& sp, const CombineParams& cp, cudaStream
             : attn_bwd_impl::make_tmap_rows(&tk, sp.K, D, sp.Lmax, heads, tc::BK) &&
                   attn_bwd_impl::make_tmap_rows(&tv, sp.V, D, sp.Lmax, heads, tc::BK);
   if (!maps) return attn_host::report(cudaErrorInvalidValue, "decode tensor maps");
-  auto kernel = tc::split_kernel<D, PAGED>;
+  auto kernel = tc::split_kernel<D, PAGED, DIFF>;
   cudaError_t e = attn_host::report(attn_host::set_smem(kernel, tc::SMEM_BYTES),
                                     "decode tensor-core kernel shared-memory attribute");
   if (e != cudaSuccess) return e;
   kernel<<<dim3(static_cast<unsigned>(sp.Hkv * sp.B), sp.nsm, 1), tc::NTHREADS, tc::SMEM_BYTES,
            s>>>(tk, tv, sp);
-  if ((e = attn_host::report_launch(kernel, "decode tensor-core split kernel")) != cudaSuccess)
-    return e;
+  return attn_host::report_launch(kernel, "decode tensor-core split kernel");
+}
+
+template <int D, bool PAGED>
+cudaError_t launch_tc(const SplitParams& sp, const CombineParams& cp, cudaStream_t s) {
+  const cudaError_t e = launch_split<D, PAGED>(sp, s);
+  if (e != cudaSuccess) return e;
   decode_combine_kernel<D><<<sp.B * sp.Hq, D, 0, s>>>(cp);
   return attn_host::report_launch(decode_combine_kernel<D>, "decode_combine_kernel");
 }
@@ -525,10 +665,11 @@ struct PagedKV {
   int max_blocks, page_log2, n_pages;
 };
 
-inline cudaError_t launch(const __nv_bfloat16* Q, const __nv_bfloat16* K, const __nv_bfloat16* V,
-                          __nv_bfloat16* O, float* lse, int B, int Hq, int Hkv, int Lmax, int d,
-                          float scale, const int* k_lens, int* status, uint8_t* scratch, int,
-                          cudaStream_t s, const PagedKV* paged = nullptr) {
+// Fields of SplitParams that the plain and the differential decode share.
+inline SplitParams split_params(const __nv_bfloat16* Q, const __nv_bfloat16* K,
+                                const __nv_bfloat16* V, int B, int Hq, int Hkv, int Lmax,
+                                float scale, const int* k_lens, int* status,
+                                const PagedKV* paged) {
   SplitParams sp;
   sp.block_table = paged ? paged->block_table : nullptr;
   sp.max_blocks = paged ? paged->max_blocks : 0;
@@ -539,16 +680,25 @@ inline cudaError_t launch(const __nv_bfloat16* Q, const __nv_bfloat16* K, const 
   sp.V = V;
   sp.k_lens = k_lens;
   sp.status = status;
-  sp.nsm = n_split_max(Lmax);
-  const size_t n = static_cast<size_t>(B) * Hq * sp.nsm;
-  sp.part_o = reinterpret_cast<float*>(scratch);
-  sp.part_lse = reinterpret_cast<float*>(scratch + n * d * 4);
   sp.B = B;
   sp.Hq = Hq;
   sp.Hkv = Hkv;
   sp.G = Hq / Hkv;
   sp.Lmax = Lmax;
   sp.scale_log2 = scale * 1.4426950408889634f;
+  return sp;
+}
+
+inline cudaError_t launch(const __nv_bfloat16* Q, const __nv_bfloat16* K, const __nv_bfloat16* V,
+                          __nv_bfloat16* O, float* lse, int B, int Hq, int Hkv, int Lmax, int d,
+                          float scale, const int* k_lens, int* status, uint8_t* scratch, int,
+                          cudaStream_t s, const PagedKV* paged = nullptr) {
+  SplitParams sp = split_params(Q, K, V, B, Hq, Hkv, Lmax, scale, k_lens, status, paged);
+  sp.ch = CH;
+  sp.nsm = n_split_max(Lmax);
+  const size_t n = static_cast<size_t>(B) * Hq * sp.nsm;
+  sp.part_o = reinterpret_cast<float*>(scratch);
+  sp.part_lse = reinterpret_cast<float*>(scratch + n * d * 4);
   CombineParams cp;
   cp.part_o = sp.part_o;
   cp.part_lse = sp.part_lse;
@@ -562,6 +712,34 @@ inline cudaError_t launch(const __nv_bfloat16* Q, const __nv_bfloat16* K, const 
   // the caller checked supported_shape()
   if (d == 128) return paged ? launch_tc<128, true>(sp, cp, s) : launch_tc<128, false>(sp, cp, s);
   return paged ? launch_tc<64, true>(sp, cp, s) : launch_tc<64, false>(sp, cp, s);
+}
+
+template <int D>
+cudaError_t launch_diff_d(const SplitParams& sp, const DiffCombineParams& cp, bool paged,
+                          cudaStream_t s) {
+  const cudaError_t e =
+      paged ? launch_split<D, true, true>(sp, s) : launch_split<D, false, true>(sp, s);
+  if (e != cudaSuccess) return e;
+  diff_combine_kernel<D><<<sp.B * sp.Hq, 32 * DC_WARPS, 0, s>>>(cp);
+  return attn_host::report_launch(diff_combine_kernel<D>, "diff_combine_kernel");
+}
+
+// Differential decode: lam [n_lam] (one weight, or one per query head), lse [B*Hq][2].
+inline cudaError_t launch_diff(const __nv_bfloat16* Q, const __nv_bfloat16* K,
+                               const __nv_bfloat16* V, const float* lam, int n_lam,
+                               __nv_bfloat16* O, float* lse, int B, int Hq, int Hkv, int Lmax,
+                               int d, float scale, const int* k_lens, int* status,
+                               uint8_t* scratch, cudaStream_t s, const PagedKV* paged) {
+  SplitParams sp = split_params(Q, K, V, B, Hq, Hkv, Lmax, scale, k_lens, status, paged);
+  sp.ch = diff_chunk(B, Hkv, Lmax);
+  sp.nsm = diff_splits(B, Hkv, Lmax);
+  const size_t n = static_cast<size_t>(B) * Hq * 2 * sp.nsm;
+  sp.part_o = reinterpret_cast<float*>(scratch);
+  sp.part_lse = reinterpret_cast<float*>(scratch + n * d * 4);
+  const DiffCombineParams cp{sp.part_o, sp.part_lse, k_lens, lam, O,     lse,
+                             Hq,        Lmax,        sp.nsm, sp.ch, n_lam};
+  return d == 128 ? launch_diff_d<128>(sp, cp, paged != nullptr, s)
+                  : launch_diff_d<64>(sp, cp, paged != nullptr, s);
 }
 
 }  // namespace attn_decode_impl

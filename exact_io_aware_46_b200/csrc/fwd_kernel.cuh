@@ -109,6 +109,11 @@ struct Params {
   // lse [B, Hq, Lq] (in/out); O (bf16, may be nullptr) receives the merged O.
   float* o_acc;
   int merge_init;  // 1: the accumulator is overwritten instead of merged into
+  // differential heads: O = O_1 - lam O_2, lse [B, Hq, 2, Lq]; O2 (may be nullptr)
+  // receives the second map's output
+  const float* lam;  // [n_lam]: one weight, or one per query head
+  int n_lam;
+  __nv_bfloat16* O2;
 };
 
 struct Item {
@@ -134,8 +139,23 @@ struct Item {
 //   MODE_WINDOW  the same with a sliding-window causal mask (p.window keys);
 //   MODE_VARLEN  packed sequences [T, H, d] with cu_seqlens offsets;
 //   MODE_FP8     the plain layout with E4M3 Q, K, V and per-tile scales;
-//   MODE_MERGE   the plain layout, the result folded into an fp32 accumulator.
-enum : int { MODE_PLAIN = 0, MODE_WINDOW = 1, MODE_VARLEN = 2, MODE_FP8 = 3, MODE_MERGE = 4 };
+//   MODE_MERGE   the plain layout, the result folded into an fp32 accumulator;
+//   MODE_DIFF    differential heads: a head row holds the halves of two maps,
+//                [q1 q2] and [k1 k2], and O = softmax(q1 k1^T) V - lam softmax(q2 k2^T) V.
+//
+// MODE_DIFF puts the two maps where the other modes have two query tiles: an item
+// is ONE 128-row query tile, S_t = Q[half t] K_j[half t]^T (half the K steps), and
+// O_t += P_t V_j, so both maps read each K and V tile once and their softmaxes
+// ping-pong as two query tiles do.  The two O stay apart until the end, when the
+// row sums are known: the four warps of a lane quarter then each combine a
+// quarter of the columns, o_1 / l_1 - lam o_2 / l_2.  6 d FLOP and two
+// exponentials per visible pair (the single sum (P_1 - lam P_2) V would need 4 d,
+// but its weights only exist once both row sums do).  K and V rows past k_len
+// may hold anything: scores are masked by selection, and V rows are cleared in
+// shared memory before the tile's PV.
+enum : int {
+  MODE_PLAIN = 0, MODE_WINDOW = 1, MODE_VARLEN = 2, MODE_FP8 = 3, MODE_MERGE = 4, MODE_DIFF = 5
+};
 
 constexpr int DEV_BAD_SCALE = 8;  // device status bit: a scale that is not finite and > 0
 
@@ -166,7 +186,7 @@ __device__ __forceinline__ Item get_item(const Params& p, int w, bool* bad) {
   const int bh = g * HEAD_GROUP + r % gsize;
   it.b = bh / p.Hq;
   it.h = bh % p.Hq;
-  it.row0 = pair * 2 * BM;
+  it.row0 = pair * (MODE == MODE_DIFF ? BM : 2 * BM);
   const int kvh = it.h / (p.Hq / p.Hkv);
   if constexpr (MODE != MODE_VARLEN) {
     int kl = p.Lk;
@@ -207,7 +227,7 @@ __device__ __forceinline__ Item get_item(const Params& p, int w, bool* bad) {
     it.lse_off = static_cast<size_t>(it.h) * p.total_q + it.q_coord;
   }
   it.n0 = tiles_for(p, it, it.row0);
-  it.n1 = tiles_for(p, it, it.row0 + BM);
+  it.n1 = MODE == MODE_DIFF ? it.n0 : tiles_for(p, it, it.row0 + BM);
   // sliding window: key tiles entirely below the first row's window are skipped
   it.lo0 = it.lo1 = 0;
   if constexpr (MODE == MODE_WINDOW) {
@@ -271,6 +291,20 @@ __device__ __forceinline__ void issue_s_tile(uint32_t d_tmem, uint32_t q_smem, u
     else
       sm100::mma_ss_f8(d_tmem, qd + off, kd + off, C::IDESC_S, k > 0 ? 1u : 0u);
   }
+}
+
+// S_t = (half t of Q) (half t of K_j)^T of a differential head: 128 x 128 x D / 2.
+template <int D>
+__device__ __forceinline__ void issue_s_half(uint32_t d_tmem, uint32_t q_smem, uint32_t k_smem,
+                                             int t) {
+  using C = Cfg<D, 2>;
+  // half t starts at column t D / 2: the second panel (d = 128) or 64 bytes into the rows
+  const uint32_t at = static_cast<uint32_t>(t) * (D == 128 ? CHUNK_BYTES : 64);
+  const uint64_t qd = sm100::sdesc_sw128(q_smem + at, 16, 1024);
+  const uint64_t kd = sm100::sdesc_sw128(k_smem + at, 16, 1024);
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k)
+    sm100::mma_ss(d_tmem, qd + 2 * k, kd + 2 * k, C::IDESC_S, k > 0 ? 1u : 0u);
 }
 
 // O_t (+)= P_t V_j: A = P_t from TMEM (8 columns per instruction: 16 keys of
@@ -338,7 +372,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       sm100::mbar_init(&s_full[t], 1);
       sm100::mbar_init(&p_full[t], NSMX / 2);  // one arrival per softmax warp of the tile
       sm100::mbar_init(&o_full[t], 1);
-      sm100::mbar_init(&o_empty[t], NSMX / 2);
+      // differential: every softmax warp reads both O
+      sm100::mbar_init(&o_empty[t], MODE == MODE_DIFF ? NSMX : NSMX / 2);
       sm100::mbar_init(&s_free[t], NSMX / 2);  // one arrival per softmax warp of the tile
       sm100::mbar_init(&p_free[t], 1);
     }
@@ -388,10 +423,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (w < 0) break;
         const Item it = get_item<D, MODE>(p, w, nullptr);
         if (!sm100::mbar_wait(q_empty, (k & 1) ^ 1, abort_flag, p.status)) break;
-        sm100::mbar_arrive_expect_tx(q_full, 2 * C::TILE_BYTES);
+        constexpr int NQT = MODE == MODE_DIFF ? 1 : 2;  // query tiles of an item
+        sm100::mbar_arrive_expect_tx(q_full, NQT * C::TILE_BYTES);
         ++q_issued;
         const int qh = it.q_head;
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < NQT; ++t)
           for (int c = 0; c < C::CHUNKS; ++c)
             sm100::tma_load_3d(&tmQ, q_full,
                                smem + C::OFF_Q + t * C::TILE_BYTES + c * CHUNK_BYTES,
@@ -448,9 +484,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
       };
       auto issue_s = [&](int t, int slot) {
-        if (leader)
-          issue_s_tile<D, EB>(tmem + C::s_col(t), q_addr + t * C::TILE_BYTES,
-                          kv_addr + slot * C::TILE_BYTES);
+        if (leader) {
+          if constexpr (MODE == MODE_DIFF)
+            issue_s_half<D>(tmem + C::s_col(t), q_addr, kv_addr + slot * C::TILE_BYTES, t);
+          else
+            issue_s_tile<D, EB>(tmem + C::s_col(t), q_addr + t * C::TILE_BYTES,
+                                kv_addr + slot * C::TILE_BYTES);
+        }
+      };
+      // differential: V rows at and past the sequence's end (kv_len < Lk) are cleared
+      // in the tile that holds it; the whole warp, 16 bytes a lane
+      auto clear_v_tail = [&](int slot, int from) {
+        uint8_t* v = smem + C::OFF_KV + slot * C::TILE_BYTES;
+        for (int e = from * 8 + sm100::lane_id(); e < BN * 8; e += 32)
+          for (int c = 0; c < C::CHUNKS; ++c)
+            *reinterpret_cast<uint4*>(v + c * CHUNK_BYTES + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+        sm100::fence_proxy_async_smem();
+        __syncwarp();
       };
       auto issue_pv = [&](int t, int slot, bool acc) {
         if (leader)
@@ -514,6 +564,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (!(ok = sm100::mbar_wait(&kv_full[vs], (vuse / C::NS) & 1, abort_flag, p.status)))
             break;
           sm100::tc_fence_after();
+          if constexpr (MODE == MODE_DIFF)
+            if (it.kv_len < p.Lk && it.kv_len < (j + 1) * BN) clear_v_tail(vs, it.kv_len - j * BN);
           // one query tile's step: O_t += P_t V_j, then S_t = Q_t K_{j+1}^T
           auto step = [&](int t, int n_t, uint32_t& pc, bool pv, bool sn) -> bool {
             auto do_pv = [&]() -> bool {
@@ -602,7 +654,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const Item it = get_item<D, MODE>(p, w, &bad);
       if (bad && threadIdx.x == 0) atomicOr(p.status, 1);
       const int n_t = t ? it.n1 : it.n0;
-      const int row0 = it.row0 + t * BM;
+      const int row0 = it.row0 + (MODE == MODE_DIFF ? 0 : t * BM);
       const int row = row0 + r;
       const int diag = row + it.koff;  // last visible key under the causal mask
       float m_use = -INFINITY, l = 0.f;
@@ -757,8 +809,74 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!ok) break;
       // ---------------- epilogue: O = o / l (bf16), LSE = ln(2) * (m + log2 l)
       if (!(ok = sm100::mbar_wait(&o_full[t], k & 1, abort_flag, p.status))) break;
+      if constexpr (MODE == MODE_DIFF)
+        if (!(ok = sm100::mbar_wait(&o_full[t ^ 1], k & 1, abort_flag, p.status))) break;
       sm100::tc_fence_after();
       const bool live = row < it.lq;
+      if constexpr (MODE == MODE_DIFF) {
+        // both maps' row sums, each the sum of its two key halves: [map][half][row]
+        constexpr int DQ = D / 4;  // columns this thread combines
+        const int cq = (t * 2 + hf) * DQ;
+        float* lx = lsum_x + (e_cnt & 1) * 4 * BM;
+        ++e_cnt;
+        lx[(t * 2 + hf) * BM + r] = l;
+        sm100::named_bar_sync(9 + qd, 128);  // the four warps of these rows
+        const float l0 = lx[r] + lx[BM + r], l1 = lx[2 * BM + r] + lx[3 * BM + r];
+        const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
+        const float lam = __ldg(p.lam + (p.n_lam == 1 ? 0 : it.h));
+        const size_t rix = (static_cast<size_t>(it.b) * p.Hq + it.h) * p.Lq + (live ? row : 0);
+        const bool wide = ((reinterpret_cast<uintptr_t>(p.O) |
+                            reinterpret_cast<uintptr_t>(p.O2)) & 31) == 0;
+        auto store = [&](__nv_bfloat16* dst, const uint32_t* pk) {
+          if (wide) {
+            st_global_v8(dst, pk);
+          } else {
+            uint4* d4 = reinterpret_cast<uint4*>(dst);
+            d4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          }
+        };
+        const bool any = n_t > 0 && l0 > 0.f;  // the row sees a key (both maps see the same)
+#pragma unroll 1
+        for (int c = cq; c < cq + DQ; c += 16) {
+          uint32_t o0[16], o1[16];
+          if (n_t > 0) {  // warp-uniform: the TMEM loads are collective
+            sm100::tmem_ld16(tmem + lane_base + C::o_col(0) + c, o0);
+            sm100::tmem_ld16(tmem + lane_base + C::o_col(1) + c, o1);
+            sm100::tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o0[e] = o1[e] = 0u;
+          }
+          uint32_t w[8], w2[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float b0 = __uint_as_float(o1[2 * e]) * i1, b1 = __uint_as_float(o1[2 * e + 1]) * i1;
+            const float a0 = __uint_as_float(o0[2 * e]) * i0 - lam * b0;
+            const float a1 = __uint_as_float(o0[2 * e + 1]) * i0 - lam * b1;
+            w[e] = any ? sm100::pack_bf16x2(a0, a1) : 0u;
+            w2[e] = any ? sm100::pack_bf16x2(b0, b1) : 0u;
+          }
+          if (live) {
+            store(p.O + rix * D + c, w);
+            if (p.O2) store(p.O2 + rix * D + c, w2);
+          }
+        }
+        if (live) {
+          if (p.lse && hf == 0) {
+            const float lt = t ? l1 : l0;
+            p.lse[((static_cast<size_t>(it.b) * p.Hq + it.h) * 2 + t) * p.Lq + row] =
+                lt > 0.f ? (m_use + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+          }
+        }
+        sm100::tc_fence_before();
+        __syncwarp();
+        if (sm100::lane_id() == 0) {
+          sm100::mbar_arrive(&o_empty[0]);
+          sm100::mbar_arrive(&o_empty[1]);
+        }
+        continue;
+      }
       // folding: both warps of a row read the accumulator's LSE before the
       // row-sum exchange below, which orders the write of the new LSE after it
       float lse_a = -INFINITY;

@@ -190,6 +190,29 @@ attn_status_t attn_bwd_sliding(const attn_bf16_t* Q, const attn_bf16_t* K, const
                                const int32_t* k_lens, void* workspace, size_t ws_bytes,
                                void* stream);
 
+/* ------------------------------------------------------------------ differential attention
+ * The difference of two softmax maps over one V with a learned weight per head
+ * (no counterpart in the pages): a head row of d elements holds the halves of
+ * two maps, Q = [q1 q2] and K = [k1 k2], each d / 2 wide, and
+ *   P_m = softmax(scale q_m k_m^T + M),  O_m = P_m V  (m = 1, 2),
+ *   O   = O_1 - lam[h] O_2,   lse[b,h,m,i] = log-sum-exp of row i of map m.
+ * The customary scale is 1/sqrt(d / 2).
+ *
+ *   lam: device fp32 [n_lam], n_lam = 1 (one weight for all heads) or Hq.
+ *   O [B,Hq,Lq,d] bf16.  O2 [B,Hq,Lq,d] bf16 (O_2, for the backward; may be
+ *   NULL).  lse [B,Hq,2,Lq] fp32 (may be NULL).  d = 64 or 128.  The other
+ *   arguments, masks and errors as attn_fwd; a row that sees no key gets O = 0,
+ *   O2 = 0 and both lse = -inf.  K and V rows at and past k_lens[b] are not used
+ *   and may hold anything.  More than 2^30 128-row tiles over all heads return
+ *   ATTN_ERR_UNSUPPORTED.
+ */
+size_t attn_fwd_diff_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk, int d);
+attn_status_t attn_fwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const attn_bf16_t* V,
+                            const float* lam, int n_lam, attn_bf16_t* O, attn_bf16_t* O2,
+                            float* lse, int B, int Hq, int Hkv, int Lq, int Lk, int d,
+                            float scale, int mask_flags, const int32_t* k_lens, void* workspace,
+                            size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ packed forward
  * The forward over variable-length sequences packed back to back (no padding):
  * the same attention per sequence as attn_fwd, with the batch given by
@@ -266,6 +289,70 @@ attn_status_t attn_fwd_splitkv_decode_paged(const attn_bf16_t* Q, const attn_bf1
                                             float* lse, int B, int Hq, int Hkv, int d,
                                             float scale, const int32_t* k_lens,
                                             void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ differential decode
+ * attn_fwd_diff for one new token per sequence (Lq = 1, no causal mask inside the
+ * cache), split over the cache's length and joined: the layouts, limits and
+ * errors of attn_fwd_splitkv_decode and attn_fwd_splitkv_decode_paged, except
+ *   lam, n_lam as attn_fwd_diff; lse [B,Hq,2] fp32 (may be NULL); Hq / Hkv at
+ *   most 8 (any number); the split length goes by B, Hkv and the cache's
+ *   capacity, so the workspace is attn_decode_diff_workspace_size(B, Hq, Hkv,
+ *   Lmax, d) bytes (Lmax = max_blocks * page_size for a paged cache).
+ * Cache rows at and past k_lens[b] are not used and may hold anything.
+ */
+size_t attn_decode_diff_workspace_size(int B, int Hq, int Hkv, int Lmax, int d);
+attn_status_t attn_fwd_splitkv_decode_diff(const attn_bf16_t* Q, const attn_bf16_t* Kcache,
+                                           const attn_bf16_t* Vcache, const float* lam, int n_lam,
+                                           attn_bf16_t* O, float* lse, int B, int Hq, int Hkv,
+                                           int Lmax, int d, float scale, const int32_t* k_lens,
+                                           void* workspace, size_t ws_bytes, void* stream);
+attn_status_t attn_fwd_splitkv_decode_diff_paged(
+    const attn_bf16_t* Q, const attn_bf16_t* Kpages, const attn_bf16_t* Vpages,
+    const int32_t* block_table, int max_blocks, int page_size, int n_pages, const float* lam,
+    int n_lam, attn_bf16_t* O, float* lse, int B, int Hq, int Hkv, int d, float scale,
+    const int32_t* k_lens, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ append to a paged cache
+ * Writes new tokens' keys and values into the pages that the paged decodes
+ * read, applying the rotary position rotation to K, and to Q on its way to the
+ * attention (no counterpart in the pages).
+ *
+ *   K, V [T,Hkv,d] and Q [T,Hq,d] bf16: the new tokens, packed sequence after
+ *   sequence.  Consecutive tokens are k_stride, v_stride and q_stride elements
+ *   apart (multiples of 8), so the views of one fused projection can be passed;
+ *   a token's head rows are contiguous.  Q and Q_out [T,Hq,d] (contiguous) may
+ *   both be NULL; Q_out may be Q itself when q_stride = Hq * d.
+ *   cu_seqlens: device int32 [B + 1] from 0, non-decreasing, at most T: sequence b's
+ *   new tokens are [cu[b], cu[b+1]).  Tokens from cu[B] on are left alone (a
+ *   buffer padded for replay).  NULL: one token per sequence, T = B.
+ *   k_lens: device int32 [B], the lengths AFTER the append (the k_lens of the
+ *   decode that follows): the n_b new tokens become rows and positions
+ *   k_lens[b] - n_b ... k_lens[b] - 1.
+ *   Kpages, Vpages, block_table, max_blocks, page_size, n_pages: the cache, as
+ *   attn_fwd_splitkv_decode_paged.  Pages and rows that take no token keep their
+ *   contents; two sequences must not append to the same page.
+ *   Rotation: each of a head row's `maps` parts (1, or 2 for differential heads)
+ *   of d / maps elements is rotated by itself, its first rope_dim elements in
+ *   pairs (i, i + rope_dim / 2), or (2 i, 2 i + 1) with interleaved = 1:
+ *     y_a = x_a cos - x_b sin,  y_b = x_b cos + x_a sin,
+ *   with cos = cos_table[row, i], sin = sin_table[row, i], device fp32
+ *   [n_pos, rope_dim / 2].  rope_dim is a multiple of 16 up to d / maps, or 0 (no
+ *   rotation, tables may be NULL); else ATTN_ERR_UNSUPPORTED.  d = 64 or 128.
+ *   Device errors: a sequence whose offsets break the rules, whose k_lens entry is
+ *   below n_b or above the cache's capacity, or a row past n_pos, sets
+ *   ATTN_DEV_BAD_KLEN; a block-table entry outside [0, n_pages) sets
+ *   ATTN_DEV_BAD_PAGE.  The tokens concerned write nothing, Q_out included.
+ */
+size_t attn_kv_append_paged_workspace_size(void);
+attn_status_t attn_kv_append_paged(const attn_bf16_t* Q, long long q_stride, const attn_bf16_t* K,
+                                   long long k_stride, const attn_bf16_t* V, long long v_stride,
+                                   attn_bf16_t* Q_out, attn_bf16_t* Kpages, attn_bf16_t* Vpages,
+                                   const int32_t* block_table, int max_blocks, int page_size,
+                                   int n_pages, const int32_t* cu_seqlens, const int32_t* k_lens,
+                                   int B, int T, int Hq, int Hkv, int d, const float* cos_table,
+                                   const float* sin_table, int n_pos, int rope_dim, int maps,
+                                   int interleaved, void* workspace, size_t ws_bytes,
+                                   void* stream);
 
 /* ------------------------------------------------------------------ backward
  * Backward by recomputation: the three-ledgers page says the backward keeps only small row
