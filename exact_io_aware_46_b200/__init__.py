@@ -21,6 +21,7 @@ The functions carry the C entry points' names:
   attention's partial results (``exact_io_aware_46_b200.ring`` drives them)
 * ``attn_fwd_diff(Q, K, V, lam, ...) -> (O, O2, LSE)``: differential attention (two softmax
   maps a head, subtracted with a learned weight)
+* ``attn_bwd_diff(Q, K, V, lam, O, O2, dO, LSE, ...) -> (dQ, dK, dV, dlam)``: its gradients
 * ``attn_fwd_splitkv_decode_diff`` / ``attn_fwd_splitkv_decode_diff_paged(...) -> (O, LSE)``: the
   same for one new token per sequence over a cache
 * ``attn_kv_append_paged(K, V, Kpages, Vpages, block_table, k_lens, ...)``: new tokens' keys and
@@ -90,6 +91,9 @@ SIGNATURES = {
     "attn_fwd_diff_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "attn_fwd_diff": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i,
                            _vp, _vp, _sz, _vp]),
+    "attn_bwd_diff_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "attn_bwd_diff": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i,
+                           _i, _i, _i, _i, _f, _i, _vp, _vp, _sz, _vp]),
     "attn_decode_diff_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "attn_fwd_splitkv_decode_diff": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
                                           _f, _vp, _vp, _sz, _vp]),
@@ -664,6 +668,46 @@ def attn_fwd_diff(Q, K, V, lam, scale=None, causal=False, k_lens=None, O=None, O
                                    workspace.numel(), handle)
     _check(code, "attn_fwd_diff")
     return O, O2, lse
+
+
+def attn_bwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d) -> int:
+    return int(lib().attn_bwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d))
+
+
+def attn_bwd_diff(Q, K, V, lam, O, O2, dO, lse, scale=None, causal=False, k_lens=None, dQ=None,
+                  dK=None, dV=None, dlam=None, workspace=None, stream=None):
+    """Backward of attn_fwd_diff, from its O, O2 and LSE.  Returns (dQ, dK, dV, dlam), bf16
+    like every gradient here; dlam has lam's shape (one shared weight gets the heads' sum)."""
+    B, Hq, Hkv, Lq, Lk, d, dev = _qkv(Q, K, V)
+    n_lam = _lam(lam, Hq, dev)
+    for t, name in ((O, "O"), (O2, "O2"), (dO, "dO")):
+        _need(t, name, torch.bfloat16, (B, Hq, Lq, d), dev)
+    _need(lse, "lse", torch.float32, (B, Hq, 2, Lq), dev)
+    _klens(k_lens, B, dev)
+    _opt(dQ, "dQ", torch.bfloat16, (B, Hq, Lq, d), dev)
+    _opt(dK, "dK", torch.bfloat16, (B, Hkv, Lk, d), dev)
+    _opt(dV, "dV", torch.bfloat16, (B, Hkv, Lk, d), dev)
+    _opt(dlam, "dlam", torch.bfloat16, (n_lam,), dev)
+    nbytes = attn_bwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d)
+    if workspace is not None:
+        _ws_check(workspace, nbytes, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d / 2)
+    with _launch_on(dev, stream) as handle:
+        if workspace is None:
+            workspace = _new_workspace(nbytes, dev, handle)
+        dQ = torch.empty_like(Q) if dQ is None else dQ
+        dK = torch.empty_like(K) if dK is None else dK
+        dV = torch.empty_like(V) if dV is None else dV
+        if dlam is None:
+            dlam = torch.empty(n_lam, dtype=torch.bfloat16, device=dev)
+        code = lib().attn_bwd_diff(_addr(Q), _addr(K), _addr(V), _addr(lam), n_lam, _addr(O),
+                                   _addr(O2), _addr(dO), _addr(lse), _addr(dQ), _addr(dK),
+                                   _addr(dV), _addr(dlam), B, Hq, Hkv, Lq, Lk, d, float(scale),
+                                   _mask(causal), _addr(k_lens), _addr(workspace),
+                                   workspace.numel(), handle)
+    _check(code, "attn_bwd_diff")
+    return dQ, dK, dV, dlam
 
 
 def _decode_diff(Q, Kc, Vc, block_table, lam, k_lens, scale, O, lse, workspace, stream, want_lse):

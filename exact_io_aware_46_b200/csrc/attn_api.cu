@@ -15,6 +15,7 @@
 #include "append_kernel.cuh"
 #include "bwd_kernel.cuh"
 #include "decode_kernel.cuh"
+#include "diff_bwd_kernel.cuh"
 #include "fwd_kernel.cuh"
 #include "launch_cache.cuh"
 #include "merge_kernel.cuh"
@@ -24,6 +25,7 @@ namespace {
 constexpr size_t kStatusBytes = 256;  // status word + scheduler counters, 256-byte aligned
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
@@ -148,6 +150,21 @@ bool attn_bwd_impl::make_tmap_acc64(CUtensorMap* m, float* base, int Lqp, long l
   if (!fn) return false;
   cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(Lqp), static_cast<cuuint64_t>(heads)};
   cuuint64_t strides[2] = {64 * 4, static_cast<cuuint64_t>(Lqp) * 64 * 4};
+  cuuint32_t box[3] = {32, 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool attn_bwd_impl::make_tmap_acc(CUtensorMap* m, float* base, int d, int Lqp, long long heads) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 4;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Lqp),
+                        static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {row, row * static_cast<cuuint64_t>(Lqp)};
   cuuint32_t box[3] = {32, 128, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
@@ -764,6 +781,66 @@ attn_status_t attn_bwd_sliding(const attn_bf16_t* Q, const attn_bf16_t* K, const
   if (window < 1) return ATTN_ERR_INVALID;
   return bwd_batched(Q, K, V, O, dO, lse, dQ, dK, dV, B, Hq, Hkv, Lq, Lk, d, scale,
                      ATTN_MASK_CAUSAL, window, k_lens, workspace, ws_bytes, stream);
+}
+
+// ------------------------------------------------------------------ differential backward
+
+size_t attn_bwd_diff_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk, int d) {
+  if (!shapes_ok(B, Hq, Hkv, Lq, Lk) || d < 0) return kStatusBytes;
+  return kStatusBytes + attn_diff_bwd_impl::scratch(B, Hq, Lq, Lk, d).total;
+}
+
+attn_status_t attn_bwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const attn_bf16_t* V,
+                            const float* lam, int n_lam, const attn_bf16_t* O,
+                            const attn_bf16_t* O2, const attn_bf16_t* dO, const float* lse,
+                            attn_bf16_t* dQ, attn_bf16_t* dK, attn_bf16_t* dV, attn_bf16_t* dlam,
+                            int B, int Hq, int Hkv, int Lq, int Lk, int d, float scale,
+                            int mask_flags, const int32_t* k_lens, void* workspace,
+                            size_t ws_bytes, void* stream) {
+  if (!shapes_ok(B, Hq, Hkv, Lq, Lk)) return ATTN_ERR_INVALID;
+  if (!lam || !dlam || !workspace) return ATTN_ERR_INVALID;
+  if (Lq > 0 && (!Q || !O || !O2 || !dO || !lse || !dQ)) return ATTN_ERR_INVALID;
+  if (Lk > 0 && (!K || !V || !dK || !dV)) return ATTN_ERR_INVALID;
+  if (n_lam != 1 && n_lam != Hq) return ATTN_ERR_INVALID;
+  const void* ptrs[] = {Q, K, V, O, O2, dO, lse, dQ, dK, dV, k_lens};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return ATTN_ERR_INVALID;  // a null pointer passes
+  if (!aligned4(lam) || !aligned2(dlam) || !aligned256(workspace)) return ATTN_ERR_INVALID;
+  if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_INVALID;
+  if (mask_flags != ATTN_MASK_NONE && mask_flags != ATTN_MASK_CAUSAL) return ATTN_ERR_INVALID;
+  if (ws_bytes < attn_bwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d)) return ATTN_ERR_INVALID;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!items_ok(B, Hq, Lq) || !items_ok(B, Hq, Lk)) return ATTN_ERR_UNSUPPORTED;
+  const int sms = device_sms();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  attn_diff_bwd_impl::Args a;
+  a.Q = reinterpret_cast<const __nv_bfloat16*>(Q);
+  a.K = reinterpret_cast<const __nv_bfloat16*>(K);
+  a.V = reinterpret_cast<const __nv_bfloat16*>(V);
+  a.O = reinterpret_cast<const __nv_bfloat16*>(O);
+  a.O2 = reinterpret_cast<const __nv_bfloat16*>(O2);
+  a.dO = reinterpret_cast<const __nv_bfloat16*>(dO);
+  a.lse = lse;
+  a.lam = lam;
+  a.n_lam = n_lam;
+  a.dQ = reinterpret_cast<__nv_bfloat16*>(dQ);
+  a.dK = reinterpret_cast<__nv_bfloat16*>(dK);
+  a.dV = reinterpret_cast<__nv_bfloat16*>(dV);
+  a.dlam = reinterpret_cast<__nv_bfloat16*>(dlam);
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.Lq = Lq;
+  a.Lk = Lk;
+  a.d = d;
+  a.scale = scale;
+  a.causal = (mask_flags & ATTN_MASK_CAUSAL) ? 1 : 0;
+  a.window = 0;
+  a.k_lens = k_lens;
+  a.status = reinterpret_cast<int*>(workspace);
+  a.scratch = reinterpret_cast<uint8_t*>(workspace) + kStatusBytes;
+  a.sms = sms;
+  return attn_diff_bwd_impl::launch(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------ status

@@ -1,0 +1,882 @@
+// diff_bwd_kernel.cuh -- backward of differential attention by recomputation.
+//
+// Head rows hold the halves of two maps, Q = [q_1 q_2], K = [k_1 k_2], over one V:
+//   P_m = exp(scale q_m k_m^T - LSE_m),  O = P_1 V - lam P_2 V,  O_2 = P_2 V.
+// With dP = dO V^T (shared by both maps) and D_m = dO . O_m (so D_2 = dO . O_2 and
+// D_1 = dO . O + lam D_2) the calculus of the definition gives
+//   dV = (P_1 - lam P_2)^T dO,   dS_1 = P_1 o (dP - D_1),  dS_2 = -lam P_2 o (dP - D_2),
+//   dq_m = scale dS_m k_m,  dk_m = scale dS_m^T q_m,  dlam = - sum P_2 o dP.
+//
+// One pass forms both maps from one read of Q, dO, K and V: five GEMMs' worth of
+// MMA work per tile, as for one map of the full width, with one dP and one dV
+// product instead of two.  Launches, work items (128 keys of one batch and
+// key/value head) and their order are those of bwd_kernel.cuh; per 128-row query
+// tile, keys on the 128 TMEM lanes (the tile's columns are query rows):
+//   S_1^T, S_2^T = K_m Q_m^T   (SS, half the K steps each, one after the other in
+//                               the same 128 columns: the softmax reads S_1 out
+//                               before S_2 is issued)
+//   dP^T = V dO^T              (SS, 128 columns)
+//   dV  += W^T dO              (TS, W = P_1 - lam P_2 in bf16 over the S columns)
+//   dK_m += dS_m^T Q_m         (SS, N = 64, dS_m staged in shared memory)
+//   dQ_m  = dS_m K_m           (SS, N = 64, lanes = query rows, over the dP columns)
+// dV (d columns) and dK (64 per map) stay in TMEM for the item: 512 columns in all.
+// At d = 64 the maps are 32 columns wide but the products still run at N = 64
+// over the whole 64-column panel -- with N this small an SS product is bound by
+// reading A -- and the half that belongs to the other map is not read.
+//
+// Warps 0-15 form P, W and dS (a key row per thread, four warps per row with 32
+// query rows each), 16-19 move dQ from TMEM through shared memory into the fp32
+// accumulator by tensor reduce-adds (staged in the dS buffers, which the products
+// have left by then: d = 128 has no shared memory to spare), 20 feeds TMA, 21
+// issues the MMAs.
+//
+// dlam needs more of P_2 than bf16 gives: its terms P_2 dP have both signs, and
+// the roundings of P_2 (2^-9 relative on average) do not shrink with the sum.
+// P_2 is therefore kept to 16 mantissa bits until dP is there.  Sums per (item, head,
+// warp) go to the workspace and are added in a fixed order, so dlam is the same
+// from run to run.
+#pragma once
+
+#include "bwd_kernel.cuh"
+
+namespace attn_bwd_impl {
+// fp32 view [heads][Lqp][d] of the dQ accumulator, boxes of 32 columns x 128 rows,
+// 128-byte swizzle (defined with the C entry points)
+bool make_tmap_acc(CUtensorMap* m, float* base, int d, int Lqp, long long heads);
+}  // namespace attn_bwd_impl
+
+namespace attn_diff_bwd_impl {
+
+using attn_bwd_impl::BMQ;
+using attn_bwd_impl::BN;
+using attn_bwd_impl::get_item;
+using attn_bwd_impl::Item;
+using attn_bwd_impl::NI;
+using attn_bwd_impl::PANEL;
+using attn_bwd_impl::st_global_v8;
+using attn_bwd_impl::tile_of;
+
+constexpr int NSMX = 16;  // P/dS warps: 4 lane quarters x 4 quarters of the query rows
+constexpr int W_DRAIN = NSMX;
+constexpr int W_LOAD = NSMX + 4;
+constexpr int W_MMA = NSMX + 5;
+constexpr int NTHREADS = 32 * (NSMX + 6);
+constexpr int ITEM_READERS = NSMX + 4 + 1;
+constexpr int NQS = 2;  // Q ring stages
+
+template <int DH>
+struct Cfg {
+  static_assert(DH == 64 || DH == 128, "head dimension");
+  static constexpr int PANELS = DH / 64;
+  static constexpr int TILE = PANELS * PANEL;
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = TILE;
+  static constexpr int OFF_Q = 2 * TILE;             // NQS stages
+  static constexpr int OFF_DO = OFF_Q + NQS * TILE;
+  static constexpr int OFF_DS = OFF_DO + TILE;       // dS_1^T, dS_2^T: two panels of 64 rows each
+  static constexpr int OFF_LD = OFF_DS + 4 * PANEL;  // -lse2_1, -lse2_2, -D_1, lam D_2: [128] each
+  static constexpr int OFF_BAR = OFF_LD + 2048;
+  static constexpr int SMEM_BYTES = OFF_BAR + 512;
+  static_assert(SMEM_BYTES <= 232448, "dynamic shared memory limit");
+  static constexpr uint32_t IDESC_DV = sm100::idesc_bf16_f32(128, DH, false, true);
+};
+constexpr uint32_t IDESC_S = sm100::idesc_bf16_f32(128, BMQ, false, false);
+constexpr uint32_t IDESC_DK = sm100::idesc_bf16_f32(128, 64, false, true);
+constexpr uint32_t IDESC_DQ = sm100::idesc_bf16_f32(128, 64, true, true);
+
+// TMEM columns
+constexpr uint32_t S_COL = 0;     // S_m^T; W^T in the first 16 of each warp's 32 columns
+constexpr uint32_t DP_COL = 128;  // dP^T, then dQ_1 and dQ_2 (64 each)
+constexpr uint32_t DV_COL = 256;
+constexpr uint32_t DK_COL = 384;  // dK_1, dK_2 (64 each)
+
+// Column pairs cp of a 16-pair block with (cp & 7) >= POLY_FROM take the FMA-pipe exp2.
+constexpr int POLY_FROM = 6;
+
+struct Params : attn_bwd_impl::Params {
+  const float* stats;  // [B*Hq][n_qt][4][128]: -lse2_1, -lse2_2, -D_1, lam D_2
+  const float* lam;    // [n_lam]
+  int n_lam;
+  float* lam_part;  // [n_items][G][NSMX] sums of P_2 dP
+};
+
+// ------------------------------------------------------------------ prep
+
+// One warp per (padded) query row: D_1, D_2, the log2-LSEs and a zeroed accumulator row.
+template <int DH>
+__global__ void __launch_bounds__(256)
+    prep_kernel(const __nv_bfloat16* O, const __nv_bfloat16* O2, const __nv_bfloat16* dO,
+                const float* lse, const float* lam, int n_lam, float* dq_acc, float* stats,
+                long long rows, int Hq, int Lq, int Lqp) {
+  constexpr int EPL = DH / 32;
+  const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const long long bh = row / Lqp;
+  const int r = static_cast<int>(row % Lqp);
+  float a1 = 0.f, a2 = 0.f;
+  if (r < Lq) {
+    const size_t off = (static_cast<size_t>(bh) * Lq + r) * DH + lane * EPL;
+    uint32_t o[EPL / 2], o2[EPL / 2], g[EPL / 2];
+#pragma unroll
+    for (int e = 0; e < EPL / 2; ++e) {
+      o[e] = reinterpret_cast<const uint32_t*>(O + off)[e];
+      o2[e] = reinterpret_cast<const uint32_t*>(O2 + off)[e];
+      g[e] = reinterpret_cast<const uint32_t*>(dO + off)[e];
+    }
+#pragma unroll
+    for (int e = 0; e < EPL / 2; ++e) {
+      const float g0 = __uint_as_float(g[e] << 16), g1 = __uint_as_float(g[e] & 0xFFFF0000u);
+      a1 += __uint_as_float(o[e] << 16) * g0 + __uint_as_float(o[e] & 0xFFFF0000u) * g1;
+      a2 += __uint_as_float(o2[e] << 16) * g0 + __uint_as_float(o2[e] & 0xFFFF0000u) * g1;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    a1 += __shfl_xor_sync(0xffffffffu, a1, o);
+    a2 += __shfl_xor_sync(0xffffffffu, a2, o);
+  }
+  float* zrow = dq_acc + static_cast<size_t>(row) * DH + lane * EPL;
+#pragma unroll
+  for (int e = 0; e < EPL; e += 2)
+    *reinterpret_cast<float2*>(zrow + e) = make_float2(0.f, 0.f);
+  if (lane < 4) {
+    const int h = static_cast<int>(bh % Hq);
+    const float l = __ldg(lam + (n_lam == 1 ? 0 : h));
+    float v;
+    if (lane < 2) {  // -inf where the row sees no key or lies past Lq: P is exactly 0
+      v = r < Lq ? -lse[(static_cast<size_t>(bh) * 2 + lane) * Lq + r] * 1.4426950408889634f
+                 : -INFINITY;
+      if (v == INFINITY) v = -INFINITY;
+    } else {
+      v = lane == 2 ? -(a1 + l * a2) : l * a2;
+    }
+    stats[(static_cast<size_t>(bh) * (Lqp / BMQ) + r / BMQ) * 512 + lane * 128 + r % BMQ] = v;
+  }
+}
+
+// dQ = bf16(scale * accumulator), four elements a thread; the blocks behind those that
+// convert add up dlam (one block per weight), each warp's sums in a fixed order.
+template <int DH>
+__global__ void __launch_bounds__(256)
+    finish_kernel(const float* dq_acc, __nv_bfloat16* dQ, long long BH, int Lq, int Lqp,
+                  float scale, long long conv_blocks, const float* lam_part, __nv_bfloat16* dlam,
+                  int B, int Hq, int Hkv, int n_kv, int n_lam) {
+  if (blockIdx.x < conv_blocks) {
+    const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const size_t total = static_cast<size_t>(BH) * Lq * (DH / 4);
+    if (i >= total) return;
+    const size_t row = i / (DH / 4);
+    const int c4 = static_cast<int>(i % (DH / 4));
+    const size_t bh = row / Lq, r = row % Lq;
+    const float4 v = reinterpret_cast<const float4*>(dq_acc + (bh * Lqp + r) * DH)[c4];
+    uint2 o;
+    o.x = sm100::pack_bf16x2(v.x * scale, v.y * scale);
+    o.y = sm100::pack_bf16x2(v.z * scale, v.w * scale);
+    reinterpret_cast<uint2*>(dQ + row * DH)[c4] = o;
+    return;
+  }
+  const int w = static_cast<int>(blockIdx.x - conv_blocks);
+  const int G = Hq / Hkv;
+  // partials [B][Hkv][n_kv][G][NSMX], read in vectors of four; n_lam == 1 adds all of them
+  constexpr int V4 = NSMX / 4;
+  const float4* part4 = reinterpret_cast<const float4*>(lam_part);
+  const long long n = static_cast<long long>(B) * n_kv * V4 * (n_lam == 1 ? Hq : 1);
+  double acc = 0.;
+#pragma unroll 4
+  for (long long e = threadIdx.x; e < n; e += 256) {
+    long long at = e;
+    if (n_lam != 1) {
+      const long long bn = e / V4;  // batch and key tile
+      const long long item = ((bn / n_kv) * Hkv + w / G) * n_kv + bn % n_kv;
+      at = (item * G + w % G) * V4 + e % V4;
+    }
+    const float4 v = part4[at];
+    acc += static_cast<double>(v.x) + v.y + v.z + v.w;
+  }
+  __shared__ double part[256];
+  part[threadIdx.x] = acc;
+  __syncthreads();
+  for (int o = 128; o >= 1; o >>= 1) {
+    if (threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) dlam[w] = __float2bfloat16_rn(static_cast<float>(-part[0]));
+}
+
+// ------------------------------------------------------------------ main
+
+template <int DH>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const __grid_constant__ CUtensorMap tmAcc, const Params p) {
+  using C = Cfg<DH>;
+  // the swizzle panels need 1024-byte alignment; at d = 128 there is no room to align by hand
+  extern __shared__ __align__(1024) uint8_t smem_diff[];
+  uint8_t* smem = smem_diff;
+  const uint32_t sbase = sm100::smem_u32(smem);
+  if (sbase & 1023) {  // never with this declaration; nothing could be computed
+    if (threadIdx.x == 0) sm100::record_timeout(p.status, 40);
+    return;
+  }
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* kv_full = bars + 0;
+  uint64_t* kv_empty = bars + 1;
+  uint64_t* q_full = bars + 2;   // [NQS]
+  uint64_t* q_empty = bars + 4;  // [NQS]
+  uint64_t* do_full = bars + 6;
+  uint64_t* do_empty = bars + 7;
+  uint64_t* l_full = bars + 8;    // both -lse2 (free again once W is out)
+  uint64_t* d_full = bars + 9;    // -D_1, lam D_2 (free again once dS is out)
+  uint64_t* s1_full = bars + 10;
+  uint64_t* s1_read = bars + 11;
+  uint64_t* s2_full = bars + 12;
+  uint64_t* w_full = bars + 13;
+  uint64_t* dp_full = bars + 14;
+  uint64_t* ds_full = bars + 15;
+  uint64_t* ds_free = bars + 16;  // the dS buffers: dQ staged there has left
+  uint64_t* dq_full = bars + 17;
+  uint64_t* dq_empty = bars + 18;  // the dP columns: dQ has left
+  uint64_t* dkv_full = bars + 19;
+  uint64_t* dkv_empty = bars + 20;
+  uint64_t* drain = bars + 21;
+  uint64_t* st_full = bars + 22;  // dQ is staged (a bounded wait, unlike a named barrier)
+  uint64_t* item_full = bars + 23;   // [NI]
+  uint64_t* item_empty = bars + 27;  // [NI]
+  int* item_ring = reinterpret_cast<int*>(bars + 31);  // [NI]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_ring + NI);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    auto init = [](uint64_t* b, uint32_t n) { sm100::mbar_init(b, n); };
+    init(kv_full, 1);
+    init(kv_empty, 1);
+    for (int s = 0; s < NQS; ++s) {
+      init(&q_full[s], 1);
+      init(&q_empty[s], 1);
+    }
+    init(do_full, 1);
+    init(do_empty, 1);
+    init(l_full, 1);
+    init(d_full, 1);
+    init(s1_full, 1);
+    init(s1_read, NSMX);
+    init(s2_full, 1);
+    init(w_full, NSMX);
+    init(dp_full, 1);
+    init(ds_full, NSMX);
+    init(ds_free, 1);
+    init(dq_full, 1);
+    init(dq_empty, 4);
+    init(dkv_full, 1);
+    init(dkv_empty, NSMX);
+    init(drain, 1);
+    init(st_full, 4);
+    for (int i = 0; i < NI; ++i) {
+      init(&item_full[i], 1);
+      init(&item_empty[i], ITEM_READERS);
+    }
+    *abort_flag = 0;
+    sm100::fence_barrier_init();
+  }
+  if (warp == W_LOAD && sm100::lane_id() == 0) {
+    sm100::prefetch_tmap(&tmQ);
+    sm100::prefetch_tmap(&tmdO);
+    sm100::prefetch_tmap(&tmK);
+    sm100::prefetch_tmap(&tmV);
+    sm100::prefetch_tmap(&tmAcc);
+  }
+  if (warp == W_MMA) {
+    sm100::tmem_alloc(tmem_slot, 512);
+    sm100::tmem_relinquish();
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int off = p.Lk - p.Lq;  // bottom-right causal alignment
+  auto wait = [&](uint64_t* b, uint32_t parity, int site) -> bool {
+    return sm100::mbar_wait(b, parity, abort_flag, p.status, site);
+  };
+  auto next_item = [&](uint32_t k, int& w) -> bool {
+    if (!wait(&item_full[k % NI], (k / NI) & 1, 41)) return false;
+    w = *reinterpret_cast<volatile int*>(&item_ring[k % NI]);
+    __syncwarp();
+    if (sm100::lane_id() == 0) sm100::mbar_arrive(&item_empty[k % NI]);
+    return true;
+  };
+
+  if (warp == W_LOAD) {
+    // ------------------------------------------------------------ TMA producer
+    // per query tile: Q into the two-stage ring, then the tile's statistics, dO and D,
+    // each into a single buffer that the tile before has left by then
+    if (sm100::lane_id() == 0) {
+      uint32_t tq = 0, ik = 0, kv_issued = 0;
+      int last_q[NQS] = {-1, -1}, last_l = -1, last_do = -1, last_d = -1;
+      bool ok = true;
+      for (; ok; ++ik) {
+        if (!(ok = wait(&item_empty[ik % NI], ((ik / NI) & 1) ^ 1, 42))) break;
+        int w = (ik == 0) ? static_cast<int>(blockIdx.x)
+                          : atomicAdd(p.sched, 1) + static_cast<int>(gridDim.x);
+        if (w >= p.n_items) w = -1;
+        *reinterpret_cast<volatile int*>(&item_ring[ik % NI]) = w;
+        sm100::mbar_arrive(&item_full[ik % NI]);
+        if (w < 0) break;
+        const Item it = get_item(p, w, nullptr);
+        if (!(ok = wait(kv_empty, (ik & 1) ^ 1, 43))) break;
+        sm100::mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+        ++kv_issued;
+        const int kvh = it.b * p.Hkv + it.hkv;
+        for (int c = 0; c < C::PANELS; ++c) {
+          sm100::tma_load_3d(&tmK, kv_full, smem + C::OFF_K + c * PANEL, c * 64, it.n * BN, kvh);
+          sm100::tma_load_3d(&tmV, kv_full, smem + C::OFF_V + c * PANEL, c * 64, it.n * BN, kvh);
+        }
+        const int nq = it.T > 0 ? it.T / p.G : 0;
+        for (int t = 0; t < it.T && ok; ++t, ++tq) {
+          int g, i;
+          tile_of(it, t, nq, g, i);
+          const int slot = tq % NQS;
+          const int qh = it.b * p.Hq + it.hkv * p.G + g;
+          const float* st = p.stats + (static_cast<size_t>(qh) * p.n_qt + i) * 512;
+          if (!(ok = wait(&q_empty[slot], ((tq / NQS) & 1) ^ 1, 44))) break;
+          sm100::mbar_arrive_expect_tx(&q_full[slot], C::TILE);
+          for (int c = 0; c < C::PANELS; ++c)
+            sm100::tma_load_3d(&tmQ, &q_full[slot], smem + C::OFF_Q + slot * C::TILE + c * PANEL,
+                               c * 64, i * BMQ, qh);
+          last_q[slot] = static_cast<int>(tq);
+          if (!(ok = wait(w_full, (tq & 1) ^ 1, 45))) break;
+          sm100::mbar_arrive_expect_tx(l_full, 1024);
+          attn_bwd_impl::bulk_g2s(smem + C::OFF_LD, st, 1024, l_full);
+          last_l = static_cast<int>(tq);
+          if (!(ok = wait(do_empty, (tq & 1) ^ 1, 46))) break;
+          sm100::mbar_arrive_expect_tx(do_full, C::TILE);
+          for (int c = 0; c < C::PANELS; ++c)
+            sm100::tma_load_3d(&tmdO, do_full, smem + C::OFF_DO + c * PANEL, c * 64, i * BMQ, qh);
+          last_do = static_cast<int>(tq);
+          if (!(ok = wait(ds_full, (tq & 1) ^ 1, 47))) break;
+          sm100::mbar_arrive_expect_tx(d_full, 1024);
+          attn_bwd_impl::bulk_g2s(smem + C::OFF_LD + 1024, st + 256, 1024, d_full);
+          last_d = static_cast<int>(tq);
+        }
+      }
+      // the CTA must not exit while copies still land in its shared memory, which an
+      // expired wait elsewhere could otherwise allow
+      if (kv_issued > 0) sm100::mbar_wait_drain(kv_full, (kv_issued - 1) & 1);
+      for (int sl = 0; sl < NQS; ++sl)
+        if (last_q[sl] >= 0) sm100::mbar_wait_drain(&q_full[sl], (last_q[sl] / NQS) & 1);
+      if (last_l >= 0) sm100::mbar_wait_drain(l_full, last_l & 1);
+      if (last_do >= 0) sm100::mbar_wait_drain(do_full, last_do & 1);
+      if (last_d >= 0) sm100::mbar_wait_drain(d_full, last_d & 1);
+    }
+  } else if (warp == W_MMA) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = sm100::elect_one();
+    uint32_t tq = 0, ik = 0;
+    bool ok = true;
+    const uint32_t kA = sbase + C::OFF_K, vA = sbase + C::OFF_V, doA = sbase + C::OFF_DO;
+    auto qA = [&](uint32_t tile) { return sbase + C::OFF_Q + (tile % NQS) * C::TILE; };
+    auto commit = [&](uint64_t* bar) {
+      if (leader) sm100::tc_commit(bar);
+      __syncwarp();
+    };
+    // S_m^T: both operands K-major, map m's half of the columns (its own panel at
+    // d = 128, 64 bytes into the rows at d = 64)
+    constexpr uint32_t HALF = DH == 128 ? PANEL : 64;
+    auto issue_s = [&](uint32_t tile, int m) {
+      const uint64_t ad = sm100::sdesc_sw128(kA + m * HALF, 16, 1024);
+      const uint64_t bd = sm100::sdesc_sw128(qA(tile) + m * HALF, 16, 1024);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < DH / 32; ++k)
+          sm100::mma_ss(tmem + S_COL, ad + 2 * k, bd + 2 * k, IDESC_S, k > 0);
+      }
+    };
+    const uint64_t do_mn = sm100::sdesc_sw128(doA, PANEL, 1024);
+    // dK_m += dS_m^T Q_m and dQ_m = dS_m K_m, eight K steps of 16 each; at d = 64 both
+    // maps multiply the one 64-column panel
+    constexpr uint32_t MPANEL = DH == 128 ? PANEL : 0;
+    auto issue_dk = [&](uint32_t tile, int m, bool first) {
+      const uint64_t ds_k = sm100::sdesc_sw128(sbase + C::OFF_DS + m * 2 * PANEL, 16, 1024);
+      const uint64_t q_mn = sm100::sdesc_sw128(qA(tile) + m * MPANEL, PANEL, 1024);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < BMQ / 16; ++k)
+          sm100::mma_ss(tmem + DK_COL + 64 * m, ds_k + ((((k >> 2) * PANEL) + (k & 3) * 32) >> 4),
+                        q_mn + ((k * 2048) >> 4), IDESC_DK, (!first || k > 0) ? 1u : 0u);
+      }
+    };
+    auto issue_dq = [&](int m) {
+      const uint64_t ds_mn = sm100::sdesc_sw128(sbase + C::OFF_DS + m * 2 * PANEL, PANEL, 1024);
+      const uint64_t k_mn = sm100::sdesc_sw128(kA + m * MPANEL, PANEL, 1024);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          sm100::mma_ss(tmem + DP_COL + 64 * m, ds_mn + ((k * 2048) >> 4),
+                        k_mn + ((k * 2048) >> 4), IDESC_DQ, k > 0 ? 1u : 0u);
+      }
+    };
+    // K and V rows at and past the sequence's end (kv_len < Lk) may hold anything:
+    // cleared, so that their zero dS and P meet zeros
+    auto clear_tail = [&](int from) {
+      for (int e = from * 8 + sm100::lane_id(); e < BN * 8; e += 32)
+        for (int c = 0; c < C::PANELS; ++c) {
+          *reinterpret_cast<uint4*>(smem + C::OFF_K + c * PANEL + e * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(smem + C::OFF_V + c * PANEL + e * 16) = make_uint4(0, 0, 0, 0);
+        }
+      sm100::fence_proxy_async_smem();
+      __syncwarp();
+    };
+    for (; ok; ++ik) {
+      int w;
+      if (!(ok = next_item(ik, w)) || w < 0) break;
+      const Item it = get_item(p, w, nullptr);
+      if (!(ok = wait(kv_full, ik & 1, 48))) break;
+      sm100::tc_fence_after();
+      if (it.T == 0) {
+        if (!(ok = wait(dkv_empty, (ik & 1) ^ 1, 49))) break;
+        commit(dkv_full);
+        commit(kv_empty);
+        continue;
+      }
+      if (it.kv_len < p.Lk && it.kv_len < (it.n + 1) * BN) clear_tail(it.kv_len - it.n * BN);
+      if (!(ok = wait(&q_full[tq % NQS], (tq / NQS) & 1, 50))) break;
+      sm100::tc_fence_after();
+      issue_s(tq, 0);
+      commit(s1_full);
+      // the products of dS(tile): both dK, both dQ; then its dS, Q and dP columns move on
+      auto issue_ds_products = [&](uint32_t tile, bool first) -> bool {
+        if (!wait(ds_full, tile & 1, 51)) return false;
+        sm100::tc_fence_after();
+        for (int m = 0; m < 2; ++m) {
+          issue_dq(m);
+          issue_dk(tile, m, first);
+        }
+        commit(dq_full);
+        commit(&q_empty[tile % NQS]);
+        return true;
+      };
+      for (int t = 0; t < it.T && ok; ++t) {
+        const uint32_t cur = tq + t;
+        const uint32_t par = cur & 1;
+        if (t > 0 && !(ok = issue_ds_products(cur - 1, t == 1))) break;
+        if (!(ok = wait(s1_read, par, 52))) break;
+        sm100::tc_fence_after();
+        issue_s(cur, 1);
+        commit(s2_full);
+        if (!(ok = wait(do_full, par, 53))) break;
+        if (!(ok = wait(dq_empty, par ^ 1, 54))) break;
+        sm100::tc_fence_after();
+        {  // dP^T = V dO^T
+          const uint64_t ad = sm100::sdesc_sw128(vA, 16, 1024);
+          const uint64_t bd = sm100::sdesc_sw128(doA, 16, 1024);
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < DH / 16; ++k) {
+              const uint64_t o = static_cast<uint64_t>(((k >> 2) * PANEL + (k & 3) * 32) >> 4);
+              sm100::mma_ss(tmem + DP_COL, ad + o, bd + o, IDESC_S, k > 0);
+            }
+          }
+        }
+        commit(dp_full);
+        if (!(ok = wait(w_full, par, 55))) break;
+        if (t == 0 && !(ok = wait(dkv_empty, (ik & 1) ^ 1, 56))) break;
+        sm100::tc_fence_after();
+        if (leader) {  // dV += W^T dO: query rows 32 c ... are 16 columns from 32 c on
+#pragma unroll
+          for (int k = 0; k < BMQ / 16; ++k)
+            sm100::mma_ts(tmem + DV_COL, tmem + S_COL + (k >> 1) * 32 + (k & 1) * 8,
+                          do_mn + ((k * 2048) >> 4), C::IDESC_DV, (t > 0 || k > 0) ? 1u : 0u);
+        }
+        commit(do_empty);
+        if (t + 1 < it.T) {
+          const uint32_t nx = cur + 1;
+          if (!(ok = wait(&q_full[nx % NQS], (nx / NQS) & 1, 57))) break;
+          sm100::tc_fence_after();
+          issue_s(nx, 0);
+          commit(s1_full);
+        }
+      }
+      if (!ok) break;
+      if (!(ok = issue_ds_products(tq + it.T - 1, it.T == 1))) break;
+      tq += it.T;
+      commit(dkv_full);
+      commit(kv_empty);
+    }
+    commit(drain);
+    sm100::mbar_wait_drain(drain, 0);
+  } else if (warp < NSMX) {
+    // ------------------------------------------------------------ P, W and dS
+    const int qd = warp & 3, cq = warp >> 2;
+    const int kl_ = qd * 32 + sm100::lane_id();  // key row within the tile = TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
+    const uint32_t s_addr = tmem + lane_base + S_COL + 32 * cq;
+    const uint32_t dp_addr = tmem + lane_base + DP_COL + 32 * cq;
+    const float4* l1v = reinterpret_cast<const float4*>(smem + C::OFF_LD + cq * 128);
+    const float4* l2v = reinterpret_cast<const float4*>(smem + C::OFF_LD + 512 + cq * 128);
+    const float4* d1v = reinterpret_cast<const float4*>(smem + C::OFF_LD + 1024 + cq * 128);
+    const float4* d2v = reinterpret_cast<const float4*>(smem + C::OFF_LD + 1536 + cq * 128);
+    uint8_t* line = smem + C::OFF_DS + (cq >> 1) * PANEL + kl_ * 128;
+    const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+    uint32_t tq = 0;
+    bool ok = true;
+    auto arrive = [&](uint64_t* bar) {
+      sm100::tc_fence_before();
+      __syncwarp();
+      if (sm100::lane_id() == 0) sm100::mbar_arrive(bar);
+    };
+    auto f2 = [](uint32_t a, uint32_t b) {
+      return make_float2(__uint_as_float(a), __uint_as_float(b));
+    };
+    for (uint32_t ik = 0; ok; ++ik) {
+      int w;
+      if (!(ok = next_item(ik, w)) || w < 0) break;
+      bool bad = false;
+      const Item it = get_item(p, w, &bad);
+      if (bad && threadIdx.x == 0) atomicOr(p.status, 1);
+      const int key = it.n * BN + kl_;
+      const int nq = it.T > 0 ? it.T / p.G : 0;
+      float* lam_part =
+          p.lam_part + ((static_cast<size_t>(it.b) * p.Hkv + it.hkv) * p.n_kv + it.n) * p.G * NSMX;
+      if (it.T == 0 && sm100::lane_id() == 0)
+        for (int g = 0; g < p.G; ++g) lam_part[g * NSMX + warp] = 0.f;
+      float2 lam_acc = make_float2(0.f, 0.f);
+      for (int t = 0; t < it.T && ok; ++t) {
+        const uint32_t par = (tq + t) & 1;
+        int g, i;
+        tile_of(it, t, nq, g, i);
+        const float lam = __ldg(p.lam + (p.n_lam == 1 ? 0 : it.hkv * p.G + g));
+        const float2 nlam = make_float2(-lam, -lam);
+        // key visible to query row r0 + c iff key < kv_len and c >= cmin
+        const bool key_ok = key < it.kv_len;
+        const int cmin = p.causal ? key - (i * BMQ + 32 * cq) - off : -1;
+        const bool all_vis = __all_sync(0xffffffffu, key_ok && cmin <= 0);
+        uint32_t s[32];
+        // scores of one map out of TMEM, masked
+        auto load_s = [&] {
+          sm100::tmem_ld32(s_addr, s);
+          sm100::tmem_ld_wait();
+        };
+        auto mask_s = [&] {
+          if (!all_vis) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!key_ok || c < cmin) s[c] = __float_as_uint(-INFINITY);
+          }
+        };
+        // exponentials of column pair cp
+        auto prob = [&](int cp, float2 nl) -> float2 {
+          const float2 x = __ffma2_rn(f2(s[2 * cp], s[2 * cp + 1]), sl2, nl);
+          if ((cp & 7) >= POLY_FROM) return sm100::ex2_poly2(x);
+          return make_float2(sm100::ex2(x.x), sm100::ex2(x.y));
+        };
+        // ---- P_1, kept in bf16
+        if (!(ok = wait(l_full, par, 58))) break;
+        if (!(ok = wait(s1_full, par, 59))) break;
+        sm100::tc_fence_after();
+        load_s();
+        arrive(s1_read);
+        mask_s();
+        uint32_t p1[16];
+#pragma unroll
+        for (int c4 = 0; c4 < 8; ++c4) {
+          const float4 nl = l1v[c4];
+          const float2 e0 = prob(2 * c4, make_float2(nl.x, nl.y));
+          const float2 e1 = prob(2 * c4 + 1, make_float2(nl.z, nl.w));
+          p1[2 * c4] = sm100::pack_bf16x2(e0.x, e0.y);
+          p1[2 * c4 + 1] = sm100::pack_bf16x2(e1.x, e1.y);
+        }
+        // ---- P_2, kept to 16 mantissa bits (upper halves of pairs, next bytes of fours),
+        // and W = P_1 - lam P_2
+        if (!(ok = wait(s2_full, par, 60))) break;
+        sm100::tc_fence_after();
+        load_s();
+        mask_s();
+        uint32_t hi[16], lo[8];
+#pragma unroll
+        for (int c4 = 0; c4 < 8; ++c4) {
+          const float4 nl = l2v[c4];
+          const float2 e0 = prob(2 * c4, make_float2(nl.x, nl.y));
+          const float2 e1 = prob(2 * c4 + 1, make_float2(nl.z, nl.w));
+          const uint32_t a = __float_as_uint(e0.x), b = __float_as_uint(e0.y);
+          const uint32_t c = __float_as_uint(e1.x), d = __float_as_uint(e1.y);
+          hi[2 * c4] = __byte_perm(a, b, 0x7632);
+          hi[2 * c4 + 1] = __byte_perm(c, d, 0x7632);
+          lo[c4] = __byte_perm(__byte_perm(a, b, 0x0051), __byte_perm(c, d, 0x0051), 0x5410);
+          const uint32_t u0 = p1[2 * c4], u1 = p1[2 * c4 + 1];
+          const float2 w0 = __ffma2_rn(e0, nlam, f2(u0 << 16, u0 & 0xFFFF0000u));
+          const float2 w1 = __ffma2_rn(e1, nlam, f2(u1 << 16, u1 & 0xFFFF0000u));
+          s[2 * c4] = sm100::pack_bf16x2(w0.x, w0.y);
+          s[2 * c4 + 1] = sm100::pack_bf16x2(w1.x, w1.y);
+        }
+        sm100::tmem_st16(s_addr, s);
+        sm100::tmem_st_wait();
+        arrive(w_full);
+        // ---- dS_1 = P_1 (dP - D_1), dS_2 = P_2 (-lam dP + lam D_2): row-contiguous per key,
+        // 16-byte chunk q of line kl_ at q ^ (kl_ & 7)
+        if (!(ok = wait(d_full, par, 61))) break;
+        if (!(ok = wait(dp_full, par, 62))) break;
+        if (!(ok = wait(ds_free, par ^ 1, 63))) break;
+        sm100::tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t dp[16];
+          sm100::tmem_ld16(dp_addr + 16 * h, dp);
+          sm100::tmem_ld_wait();
+          uint32_t w1[8], w2[8];
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) {
+            const int cc = 4 * h + c4;  // columns 4 cc ... of the thread's 32
+            const float4 n1 = d1v[cc], n2 = d2v[cc];
+            const float2 g0 = f2(dp[4 * c4], dp[4 * c4 + 1]);
+            const float2 g1 = f2(dp[4 * c4 + 2], dp[4 * c4 + 3]);
+            const uint32_t u0 = p1[2 * cc], u1 = p1[2 * cc + 1];
+            const float2 a0 = __fmul2_rn(f2(u0 << 16, u0 & 0xFFFF0000u),
+                                         __fadd2_rn(g0, make_float2(n1.x, n1.y)));
+            const float2 a1 = __fmul2_rn(f2(u1 << 16, u1 & 0xFFFF0000u),
+                                         __fadd2_rn(g1, make_float2(n1.z, n1.w)));
+            const float2 q0 = f2(__byte_perm(hi[2 * cc], lo[cc], 0x1044),
+                                 __byte_perm(hi[2 * cc], lo[cc], 0x3255));
+            const float2 q1 = f2(__byte_perm(hi[2 * cc + 1], lo[cc], 0x1066),
+                                 __byte_perm(hi[2 * cc + 1], lo[cc], 0x3277));
+            lam_acc = __ffma2_rn(q0, g0, lam_acc);
+            lam_acc = __ffma2_rn(q1, g1, lam_acc);
+            const float2 b0 = __fmul2_rn(q0, __ffma2_rn(g0, nlam, make_float2(n2.x, n2.y)));
+            const float2 b1 = __fmul2_rn(q1, __ffma2_rn(g1, nlam, make_float2(n2.z, n2.w)));
+            w1[2 * c4] = sm100::pack_bf16x2(a0.x, a0.y);
+            w1[2 * c4 + 1] = sm100::pack_bf16x2(a1.x, a1.y);
+            w2[2 * c4] = sm100::pack_bf16x2(b0.x, b0.y);
+            w2[2 * c4 + 1] = sm100::pack_bf16x2(b1.x, b1.y);
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint8_t* at = line + (((4 * (cq & 1) + 2 * h + q) ^ (kl_ & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) =
+                make_uint4(w1[4 * q], w1[4 * q + 1], w1[4 * q + 2], w1[4 * q + 3]);
+            *reinterpret_cast<uint4*>(at + 2 * PANEL) =
+                make_uint4(w2[4 * q], w2[4 * q + 1], w2[4 * q + 2], w2[4 * q + 3]);
+          }
+        }
+        sm100::fence_proxy_async_smem();
+        arrive(ds_full);
+        if ((t + 1) % nq == 0) {  // the group's next head
+          float x = lam_acc.x + lam_acc.y;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+          if (sm100::lane_id() == 0) lam_part[g * NSMX + warp] = x;
+          lam_acc = make_float2(0.f, 0.f);
+        }
+      }
+      if (!ok) break;
+      tq += it.T;
+      // ---------------- epilogue: dV, dK (x scale) of this key row, a quarter of the columns
+      if (!(ok = wait(dkv_full, ik & 1, 64))) break;
+      sm100::tc_fence_after();
+      const bool live = key < p.Lk;
+      const size_t orow = (static_cast<size_t>(it.b) * p.Hkv + it.hkv) * p.Lk + (live ? key : 0);
+      const bool wide =
+          ((reinterpret_cast<uintptr_t>(p.dV) | reinterpret_cast<uintptr_t>(p.dK)) & 31) == 0;
+      constexpr int DQ = DH / 4;
+#pragma unroll 1
+      for (int m = 0; m < 2; ++m) {
+        __nv_bfloat16* dst = (m == 0 ? p.dV : p.dK) + orow * DH + DQ * cq;
+        const float f = (m == 0) ? 1.f : p.scale;
+        // dK: map 2's half starts 64 columns on (d = 64: its own columns of a full-width product)
+        const uint32_t col = (m == 0 ? DV_COL : DK_COL + (DH == 64 ? 64 * (cq >> 1) : 0)) + DQ * cq;
+#pragma unroll 1
+        for (int c = 0; c < DQ; c += 16) {
+          uint32_t v[16], o[8];
+          sm100::tmem_ld16(tmem + lane_base + col + c, v);
+          sm100::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            o[e] = it.T > 0 ? sm100::pack_bf16x2(__uint_as_float(v[2 * e]) * f,
+                                                 __uint_as_float(v[2 * e + 1]) * f)
+                            : 0u;
+          if (live) {
+            if (wide) {
+              st_global_v8(dst + c, o);
+            } else {
+              uint4* d4 = reinterpret_cast<uint4*>(dst + c);
+              d4[0] = make_uint4(o[0], o[1], o[2], o[3]);
+              d4[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+          }
+        }
+      }
+      arrive(dkv_empty);
+    }
+  } else {
+    // ------------------------------------------------------------ dQ drain
+    // dQ_m (lanes = the tile's rows) through the dS buffer of its map, which every
+    // product has read: boxes of 128 rows x 32 columns in the 128-byte swizzle of the
+    // accumulator's tensor map, added by tensor reduce-adds
+    const int tid = threadIdx.x - 32 * W_DRAIN;  // = TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t tq = 0;
+    bool ok = true;
+    for (uint32_t ik = 0; ok; ++ik) {
+      int w;
+      if (!(ok = next_item(ik, w)) || w < 0) break;
+      const Item it = get_item(p, w, nullptr);
+      const int nq = it.T > 0 ? it.T / p.G : 0;
+      for (int t = 0; t < it.T && ok; ++t) {
+        const uint32_t cur = tq + t;
+        int g, i;
+        tile_of(it, t, nq, g, i);
+        const int qh = it.b * p.Hq + it.hkv * p.G + g;
+        if (!(ok = wait(dq_full, cur & 1, 65))) break;
+        sm100::tc_fence_after();
+        constexpr int BOXES = DH / 32;  // of both maps: box b is columns 32 b ...
+#pragma unroll
+        for (int b = 0; b < BOXES; ++b) {
+          uint32_t v[32];
+          // d = 64: map b's own 32 columns of its full-width product
+          sm100::tmem_ld32(tmem + lane_base + DP_COL + (DH == 64 ? 96 * b : 32 * b), v);
+          sm100::tmem_ld_wait();
+          uint8_t* box = smem + C::OFF_DS + b * (BMQ * 128) + tid * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(box + ((c ^ (tid & 7)) << 4)) =
+                make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        }
+        sm100::fence_proxy_async_smem();
+        sm100::tc_fence_before();
+        __syncwarp();
+        if (sm100::lane_id() == 0) {
+          sm100::mbar_arrive(dq_empty);
+          sm100::mbar_arrive(st_full);
+        }
+        if (tid == 0) {
+          if (!(ok = wait(st_full, cur & 1, 66))) break;
+          for (int b = 0; b < BOXES; ++b)
+            attn_bwd_impl::tma_reduce_add_3d(&tmAcc, smem + C::OFF_DS + b * (BMQ * 128), 32 * b,
+                                             i * BMQ, qh);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          attn_bwd_impl::bulk_wait_read_all();
+          sm100::mbar_arrive(ds_free);
+        }
+      }
+      tq += it.T;
+    }
+    // the finishing pass reads the accumulator after this kernel
+    if (tid == 0) attn_bwd_impl::bulk_wait_all();
+  }
+
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0) {
+    // the last CTA to finish re-arms the dynamic scheduler for the next launch
+    __threadfence();
+    if (atomicAdd(p.sched + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+      p.sched[0] = 0;
+      p.sched[1] = 0;
+      __threadfence();
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+struct Args : attn_bwd_impl::Args {
+  const __nv_bfloat16* O2;
+  const float* lam;
+  int n_lam;
+  __nv_bfloat16* dlam;
+};
+
+// fp32 accumulator, statistics and dlam partials
+struct Scratch {
+  size_t acc, stats, part, total;
+};
+inline Scratch scratch(int B, int Hq, int Lq, int Lk, int d) {
+  const size_t rows = static_cast<size_t>(B) * Hq * attn_bwd_impl::lq_pad(Lq);
+  const size_t n_kv = (static_cast<size_t>(Lk) + BN - 1) / BN;
+  Scratch s;
+  s.acc = 0;
+  s.stats = rows * d * 4;
+  s.part = s.stats + rows * 16;
+  s.total = (s.part + static_cast<size_t>(B) * Hq * n_kv * NSMX * 4 + 255) & ~static_cast<size_t>(255);
+  return s;
+}
+
+template <int DH>
+attn_status_t launch_d(const Args& a, cudaStream_t s) {
+  using C = Cfg<DH>;
+  Params p{};
+  const Scratch sc = scratch(a.B, a.Hq, a.Lq, a.Lk, DH);
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = a.Hq / a.Hkv;
+  p.Lq = a.Lq;
+  p.Lk = a.Lk;
+  p.Lqp = attn_bwd_impl::lq_pad(a.Lq);
+  p.scale = a.scale;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.causal = a.causal;
+  p.k_lens = a.k_lens;
+  p.status = a.status;
+  p.sched = a.status + 1;
+  p.dK = a.dK;
+  p.dV = a.dV;
+  p.n_kv = (a.Lk + BN - 1) / BN;
+  p.n_qt = p.Lqp / BMQ;
+  p.n_items = a.B * a.Hkv * p.n_kv;
+  p.dq_acc = reinterpret_cast<float*>(a.scratch + sc.acc);
+  float* stats = reinterpret_cast<float*>(a.scratch + sc.stats);
+  p.stats = stats;
+  p.lam_part = reinterpret_cast<float*>(a.scratch + sc.part);
+  p.lam = a.lam;
+  p.n_lam = a.n_lam;
+  const long long BH = static_cast<long long>(a.B) * a.Hq;
+
+  if (a.Lq > 0) {
+    const long long rows = BH * p.Lqp;
+    prep_kernel<DH><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(
+        a.O, a.O2, a.dO, a.lse, a.lam, a.n_lam, p.dq_acc, stats, rows, a.Hq, a.Lq, p.Lqp);
+    if (attn_host::report_launch(prep_kernel<DH>, "diff prep_kernel") != cudaSuccess)
+      return ATTN_ERR_CUDA;
+  }
+  if (p.n_items > 0) {
+    // Lq == 0: no query tile is loaded; the maps only need an address
+    const void* q = a.Lq > 0 ? a.Q : a.K;
+    const void* g = a.Lq > 0 ? a.dO : a.K;
+    const long long kvh = static_cast<long long>(a.B) * a.Hkv;
+    CUtensorMap tq, tdo, tk, tv, tacc;
+    if (!attn_bwd_impl::make_tmap_rows(&tq, q, DH, a.Lq, BH, BMQ) ||
+        !attn_bwd_impl::make_tmap_rows(&tdo, g, DH, a.Lq, BH, BMQ) ||
+        !attn_bwd_impl::make_tmap_rows(&tk, a.K, DH, a.Lk, kvh, BN) ||
+        !attn_bwd_impl::make_tmap_rows(&tv, a.V, DH, a.Lk, kvh, BN) ||
+        !attn_bwd_impl::make_tmap_acc(&tacc, p.dq_acc, DH, p.Lqp, BH)) {
+      attn_host::report(cudaErrorInvalidValue, "diff bwd tensor maps");
+      return ATTN_ERR_CUDA;
+    }
+    if (attn_host::report(attn_host::set_smem(main_kernel<DH>, C::SMEM_BYTES),
+                          "diff main_kernel shared-memory attribute") != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    const int grid = p.n_items < a.sms ? p.n_items : a.sms;
+    main_kernel<DH><<<grid, NTHREADS, C::SMEM_BYTES, s>>>(tq, tdo, tk, tv, tacc, p);
+    if (attn_host::report_launch(main_kernel<DH>, "diff main_kernel") != cudaSuccess)
+      return ATTN_ERR_CUDA;
+  }
+  const long long conv = (BH * a.Lq * (DH / 4) + 255) / 256;
+  finish_kernel<DH><<<static_cast<unsigned>(conv + a.n_lam), 256, 0, s>>>(
+      p.dq_acc, a.dQ, BH, a.Lq, p.Lqp, a.scale, conv, p.lam_part, a.dlam, a.B, a.Hq, a.Hkv, p.n_kv,
+      a.n_lam);
+  return attn_host::report_launch(finish_kernel<DH>, "diff finish_kernel") == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+inline attn_status_t launch(const Args& a, cudaStream_t s) {
+  return a.d == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s);
+}
+
+}  // namespace attn_diff_bwd_impl

@@ -359,6 +359,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_ring + NI);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
+  // differential: the row sums of a lane quarter's four warps are in ([4]; a bounded wait,
+  // unlike a named barrier)
+  uint64_t* l_bar = bars + 56;
+
   const int warp = threadIdx.x >> 5;
 
   if (threadIdx.x == 0) {
@@ -378,6 +382,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       sm100::mbar_init(&p_free[t], 1);
     }
     sm100::mbar_init(drain, 1);
+    if constexpr (MODE == MODE_DIFF)
+      for (int i = 0; i < 4; ++i) sm100::mbar_init(&l_bar[i], 4);
     for (int i = 0; i < NI; ++i) {
       sm100::mbar_init(&item_full[i], 1);
       sm100::mbar_init(&item_empty[i], 1 + 32 * NSMX);  // the MMA thread + all softmax threads
@@ -818,9 +824,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         constexpr int DQ = D / 4;  // columns this thread combines
         const int cq = (t * 2 + hf) * DQ;
         float* lx = lsum_x + (e_cnt & 1) * 4 * BM;
-        ++e_cnt;
         lx[(t * 2 + hf) * BM + r] = l;
-        sm100::named_bar_sync(9 + qd, 128);  // the four warps of these rows
+        __syncwarp();
+        if (sm100::lane_id() == 0) sm100::mbar_arrive(&l_bar[qd]);
+        if (!(ok = sm100::mbar_wait(&l_bar[qd], e_cnt & 1, abort_flag, p.status))) break;
+        ++e_cnt;
         const float l0 = lx[r] + lx[BM + r], l1 = lx[2 * BM + r] + lx[3 * BM + r];
         const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
         const float lam = __ldg(p.lam + (p.n_lam == 1 ? 0 : it.h));

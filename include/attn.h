@@ -213,6 +213,28 @@ attn_status_t attn_fwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const at
                             float scale, int mask_flags, const int32_t* k_lens, void* workspace,
                             size_t ws_bytes, void* stream);
 
+/* Backward of attn_fwd_diff by recomputation.  With dP = dO V^T and D_m = dO . O_m,
+ *   dV = (P_1 - lam P_2)^T dO,  dS_1 = P_1 o (dP - D_1),  dS_2 = -lam P_2 o (dP - D_2),
+ *   dq_m = scale dS_m k_m,  dk_m = scale dS_m^T q_m,  dlam = - sum P_2 o dP
+ * (dK, dV summed over the query heads of a KV head; dlam over the batch and the
+ * rows, and over the heads when n_lam = 1).
+ *   O, O2, lse as attn_fwd_diff wrote them for the same arguments; dO [B,Hq,Lq,d]
+ *   bf16, finite.  dQ [B,Hq,Lq,d], dK, dV [B,Hkv,Lk,d] and dlam [n_lam] are
+ *   written, all bf16, with dK = dV = 0 at and past k_lens[b].  Masks, limits and
+ *   errors as attn_fwd_diff.  The workspace holds the fp32 dQ accumulator, four
+ *   fp32 statistics per query row and the partial sums of dlam.  dQ's sums are
+ *   formed in no fixed order (its last bit may differ from run to run); dK, dV and
+ *   dlam are the same each time.
+ */
+size_t attn_bwd_diff_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk, int d);
+attn_status_t attn_bwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const attn_bf16_t* V,
+                            const float* lam, int n_lam, const attn_bf16_t* O,
+                            const attn_bf16_t* O2, const attn_bf16_t* dO, const float* lse,
+                            attn_bf16_t* dQ, attn_bf16_t* dK, attn_bf16_t* dV, attn_bf16_t* dlam,
+                            int B, int Hq, int Hkv, int Lq, int Lk, int d, float scale,
+                            int mask_flags, const int32_t* k_lens, void* workspace,
+                            size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ packed forward
  * The forward over variable-length sequences packed back to back (no padding):
  * the same attention per sequence as attn_fwd, with the batch given by
