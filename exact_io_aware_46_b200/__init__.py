@@ -31,8 +31,8 @@ The functions carry the C entry points' names:
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -117,6 +117,8 @@ class AttnError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded C library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -168,6 +170,9 @@ _DTYPE_NAMES = {torch.bfloat16: "bfloat16", torch.float32: "float32", torch.int3
 def _need(t, name, dtype, shape=None, device=None):
     """``t`` must be a contiguous CUDA tensor of ``dtype`` (and ``shape`` and
     ``device`` when given)."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (device is None or t.device == device)):
+        return t  # a small call costs about as much as its checks: the sound case first
     if t is None:
         raise ValueError(f"{name} is required")
     if not getattr(t, "is_cuda", False):
@@ -200,7 +205,7 @@ def _qkv(Q, K, V, dtype=torch.bfloat16, names=("Q", "K", "V")):
     _need(Q, names[0], dtype)
     if Q.dim() != 4:
         raise ValueError(f"{names[0]} must be [B, H, L, d], got {tuple(Q.shape)}")
-    B, Hq, Lq, d = (int(x) for x in Q.shape)
+    B, Hq, Lq, d = Q.shape
     dev = Q.device
     _need(K, names[1], dtype, device=dev)
     if K.dim() != 4 or int(K.shape[0]) != B or int(K.shape[3]) != d:
@@ -486,7 +491,7 @@ def _decode_args(Q, Kc, Vc, k_lens, O, lse, kv_names=("Kcache", "Vcache")):
     _need(Q, "Q", torch.bfloat16)
     if Q.dim() != 4 or int(Q.shape[2]) != 1:
         raise ValueError(f"Q must be [B, Hq, 1, d], got {tuple(Q.shape)}")
-    B, Hq, _, d = (int(x) for x in Q.shape)
+    B, Hq, _, d = Q.shape
     dev = Q.device
     _need(Kc, kv_names[0], torch.bfloat16, device=dev)
     if Kc.dim() != 4 or int(Kc.shape[3]) != d:
@@ -593,23 +598,32 @@ def attn_bwd(Q, K, V, O, dO, lse, scale=None, causal=False, k_lens=None, dQ=None
 # ------------------------------------------------------------------ differential attention
 
 
-@contextlib.contextmanager
-def _launch_on(dev, stream):
-    """Runs a call on ``stream`` (default: the current stream of the tensors' device): what it
-    allocates belongs to that stream, and the tensors' device is current meanwhile.  Yields
-    the stream's handle."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
-    else:
+def _launch(dev, stream, call):
+    """``call(handle)`` on ``stream`` (default: the current stream of the tensors' device):
+    what it allocates belongs to that stream, and the tensors' device is current meanwhile."""
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            return call(_raw_stream(dev.index))
         with torch.cuda.device(dev):
-            yield torch.cuda.current_stream(dev).cuda_stream
+            return call(_raw_stream(dev.index))
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+try:  # the same handle without a Stream object around it (a microsecond of a small call)
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream  # noqa: F811
+except ImportError:
+    pass
 
 
 def _new_workspace(nbytes, dev, handle):
@@ -625,10 +639,12 @@ def _lam(lam, Hq, dev):
     return int(lam.numel())
 
 
+@functools.lru_cache(maxsize=256)
 def attn_fwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d) -> int:
     return int(lib().attn_fwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d))
 
 
+@functools.lru_cache(maxsize=256)
 def attn_decode_diff_workspace_size(B, Hq, Hkv, Lmax, d) -> int:
     return int(lib().attn_decode_diff_workspace_size(B, Hq, Hkv, Lmax, d))
 
@@ -651,25 +667,25 @@ def attn_fwd_diff(Q, K, V, lam, scale=None, causal=False, k_lens=None, O=None, O
     nbytes = attn_fwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d)
     if workspace is not None:
         _ws_check(workspace, nbytes, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d / 2)
-    with _launch_on(dev, stream) as handle:
-        if workspace is None:
-            workspace = _new_workspace(nbytes, dev, handle)
-        if O is None:
-            O = torch.empty_like(Q)
-        if want_aux:
-            O2 = torch.empty_like(Q) if O2 is None else O2
-            if lse is None:
-                lse = torch.empty((B, Hq, 2, Lq), dtype=torch.float32, device=dev)
-        code = lib().attn_fwd_diff(_addr(Q), _addr(K), _addr(V), _addr(lam), n_lam, _addr(O),
-                                   _addr(O2), _addr(lse), B, Hq, Hkv, Lq, Lk, d, float(scale),
-                                   _mask(causal), _addr(k_lens), _addr(workspace),
-                                   workspace.numel(), handle)
-    _check(code, "attn_fwd_diff")
-    return O, O2, lse
+    scale = 1.0 / math.sqrt(d / 2) if scale is None else float(scale)
+
+    def call(handle):
+        ws = _new_workspace(nbytes, dev, handle) if workspace is None else workspace
+        o = torch.empty_like(Q) if O is None else O
+        o2 = torch.empty_like(Q) if want_aux and O2 is None else O2
+        ls = lse
+        if want_aux and ls is None:
+            ls = torch.empty((B, Hq, 2, Lq), dtype=torch.float32, device=dev)
+        _check(lib().attn_fwd_diff(Q.data_ptr(), K.data_ptr(), V.data_ptr(), lam.data_ptr(), n_lam,
+                                   o.data_ptr(), _addr(o2), _addr(ls), B, Hq, Hkv, Lq, Lk, d,
+                                   scale, _mask(causal), _addr(k_lens), ws.data_ptr(), ws.numel(),
+                                   handle), "attn_fwd_diff")
+        return o, o2, ls
+
+    return _launch(dev, stream, call)
 
 
+@functools.lru_cache(maxsize=256)
 def attn_bwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d) -> int:
     return int(lib().attn_bwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d))
 
@@ -691,23 +707,22 @@ def attn_bwd_diff(Q, K, V, lam, O, O2, dO, lse, scale=None, causal=False, k_lens
     nbytes = attn_bwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d)
     if workspace is not None:
         _ws_check(workspace, nbytes, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d / 2)
-    with _launch_on(dev, stream) as handle:
-        if workspace is None:
-            workspace = _new_workspace(nbytes, dev, handle)
-        dQ = torch.empty_like(Q) if dQ is None else dQ
-        dK = torch.empty_like(K) if dK is None else dK
-        dV = torch.empty_like(V) if dV is None else dV
-        if dlam is None:
-            dlam = torch.empty(n_lam, dtype=torch.bfloat16, device=dev)
-        code = lib().attn_bwd_diff(_addr(Q), _addr(K), _addr(V), _addr(lam), n_lam, _addr(O),
-                                   _addr(O2), _addr(dO), _addr(lse), _addr(dQ), _addr(dK),
-                                   _addr(dV), _addr(dlam), B, Hq, Hkv, Lq, Lk, d, float(scale),
-                                   _mask(causal), _addr(k_lens), _addr(workspace),
-                                   workspace.numel(), handle)
-    _check(code, "attn_bwd_diff")
-    return dQ, dK, dV, dlam
+    scale = 1.0 / math.sqrt(d / 2) if scale is None else float(scale)
+
+    def call(handle):
+        ws = _new_workspace(nbytes, dev, handle) if workspace is None else workspace
+        dq = torch.empty_like(Q) if dQ is None else dQ
+        dk = torch.empty_like(K) if dK is None else dK
+        dv = torch.empty_like(V) if dV is None else dV
+        dl = torch.empty(n_lam, dtype=torch.bfloat16, device=dev) if dlam is None else dlam
+        _check(lib().attn_bwd_diff(Q.data_ptr(), K.data_ptr(), V.data_ptr(), lam.data_ptr(), n_lam,
+                                   O.data_ptr(), O2.data_ptr(), dO.data_ptr(), lse.data_ptr(),
+                                   dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dl.data_ptr(), B,
+                                   Hq, Hkv, Lq, Lk, d, scale, _mask(causal), _addr(k_lens),
+                                   ws.data_ptr(), ws.numel(), handle), "attn_bwd_diff")
+        return dq, dk, dv, dl
+
+    return _launch(dev, stream, call)
 
 
 def _decode_diff(Q, Kc, Vc, block_table, lam, k_lens, scale, O, lse, workspace, stream, want_lse):
@@ -734,28 +749,27 @@ def _decode_diff(Q, Kc, Vc, block_table, lam, k_lens, scale, O, lse, workspace, 
     nbytes = attn_decode_diff_workspace_size(B, Hq, Hkv, Lmax, d)
     if workspace is not None:
         _ws_check(workspace, nbytes, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d / 2)
-    with _launch_on(dev, stream) as handle:
-        if workspace is None:
-            workspace = _new_workspace(nbytes, dev, handle)
-        if O is None:
-            O = torch.empty_like(Q)
-        if lse is None and want_lse:
-            lse = torch.empty((B, Hq, 2), dtype=torch.float32, device=dev)
-        tail = (d, float(scale), _addr(k_lens), _addr(workspace), workspace.numel(), handle)
+    scale = 1.0 / math.sqrt(d / 2) if scale is None else float(scale)
+
+    def call(handle):
+        ws = _new_workspace(nbytes, dev, handle) if workspace is None else workspace
+        o = torch.empty_like(Q) if O is None else O
+        ls = lse
+        if ls is None and want_lse:
+            ls = torch.empty((B, Hq, 2), dtype=torch.float32, device=dev)
+        tail = (d, scale, k_lens.data_ptr(), ws.data_ptr(), ws.numel(), handle)
         if paged:
-            name = "attn_fwd_splitkv_decode_diff_paged"
-            code = lib().attn_fwd_splitkv_decode_diff_paged(
-                _addr(Q), _addr(Kc), _addr(Vc), _addr(block_table), max_blocks, rows,
-                int(Kc.shape[0]), _addr(lam), n_lam, _addr(O), _addr(lse), B, Hq, Hkv, *tail)
+            _check(lib().attn_fwd_splitkv_decode_diff_paged(
+                Q.data_ptr(), Kc.data_ptr(), Vc.data_ptr(), block_table.data_ptr(), max_blocks,
+                rows, Kc.shape[0], lam.data_ptr(), n_lam, o.data_ptr(), _addr(ls), B, Hq, Hkv,
+                *tail), "attn_fwd_splitkv_decode_diff_paged")
         else:
-            name = "attn_fwd_splitkv_decode_diff"
-            code = lib().attn_fwd_splitkv_decode_diff(
-                _addr(Q), _addr(Kc), _addr(Vc), _addr(lam), n_lam, _addr(O), _addr(lse), B, Hq,
-                Hkv, Lmax, *tail)
-    _check(code, name)
-    return O, lse
+            _check(lib().attn_fwd_splitkv_decode_diff(
+                Q.data_ptr(), Kc.data_ptr(), Vc.data_ptr(), lam.data_ptr(), n_lam, o.data_ptr(),
+                _addr(ls), B, Hq, Hkv, Lmax, *tail), "attn_fwd_splitkv_decode_diff")
+        return o, ls
+
+    return _launch(dev, stream, call)
 
 
 def attn_fwd_splitkv_decode_diff(Q, Kc, Vc, lam, k_lens, scale=None, O=None, lse=None,
@@ -779,6 +793,7 @@ def attn_fwd_splitkv_decode_diff_paged(Q, Kp, Vp, block_table, lam, k_lens, scal
 # ------------------------------------------------------------------ append to a paged cache
 
 
+@functools.lru_cache(maxsize=1)
 def attn_kv_append_paged_workspace_size() -> int:
     return int(lib().attn_kv_append_paged_workspace_size())
 
@@ -786,6 +801,12 @@ def attn_kv_append_paged_workspace_size() -> int:
 def _tokens(t, name, d, dev, heads=None, T=None):
     """New tokens [T, H, d] bf16 whose head rows are contiguous within a token (any token
     stride that is a multiple of 8: views of a fused projection).  Returns (T, H, stride)."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.bfloat16 and t.dim() == 3 \
+            and t.device == dev:
+        (t0, h0, d0), (s0, s1, s2) = t.shape, t.stride()
+        if d0 == d and s2 == 1 and s1 == d and s0 % 8 == 0 and s0 >= h0 * d and t0 > 0 \
+                and (heads is None or h0 == heads) and (T is None or t0 == T):
+            return t0, h0, s0  # the sound case first
     if t is None:
         raise ValueError(f"{name} is required")
     if not getattr(t, "is_cuda", False):
@@ -825,7 +846,7 @@ def attn_kv_append_paged(K, V, Kp, Vp, block_table, k_lens, cu_seqlens=None, Q=N
     _need(Kp, "Kpages", torch.bfloat16)
     if Kp.dim() != 4:
         raise ValueError(f"Kpages must be [n_pages, Hkv, page, d], got {tuple(Kp.shape)}")
-    n_pages, Hkv, page, d = (int(x) for x in Kp.shape)
+    n_pages, Hkv, page, d = Kp.shape
     dev = Kp.device
     _need(Vp, "Vpages", torch.bfloat16, (n_pages, Hkv, page, d), dev)
     T, _, ks = _tokens(K, "K", d, dev, Hkv)
@@ -862,15 +883,18 @@ def attn_kv_append_paged(K, V, Kp, Vp, block_table, k_lens, cu_seqlens=None, Q=N
     nbytes = attn_kv_append_paged_workspace_size()
     if workspace is not None:
         _ws_check(workspace, nbytes, dev)
-    with _launch_on(dev, stream) as handle:
-        if workspace is None:
-            workspace = _new_workspace(nbytes, dev, handle)
-        if Q is not None and Q_out is None:
-            Q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
-        code = lib().attn_kv_append_paged(
-            _addr(Q), qs, _addr(K), ks, _addr(V), vs, _addr(Q_out), _addr(Kp), _addr(Vp),
-            _addr(block_table), int(block_table.shape[1]), page, n_pages, _addr(cu_seqlens),
-            _addr(k_lens), B, T, Hq, Hkv, d, _addr(cos), _addr(sin), n_pos, rope, int(maps),
-            1 if interleaved else 0, _addr(workspace), workspace.numel(), handle)
-    _check(code, "attn_kv_append_paged")
-    return Q_out
+
+    def call(handle):
+        ws = _new_workspace(nbytes, dev, handle) if workspace is None else workspace
+        qo = Q_out
+        if Q is not None and qo is None:
+            qo = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        _check(lib().attn_kv_append_paged(
+            _addr(Q), qs, K.data_ptr(), ks, V.data_ptr(), vs, _addr(qo), Kp.data_ptr(),
+            Vp.data_ptr(), block_table.data_ptr(), block_table.shape[1], page, n_pages,
+            _addr(cu_seqlens), k_lens.data_ptr(), B, T, Hq, Hkv, d, _addr(cos), _addr(sin), n_pos,
+            rope, maps, 1 if interleaved else 0, ws.data_ptr(), ws.numel(), handle),
+            "attn_kv_append_paged")
+        return qo
+
+    return _launch(dev, stream, call)
