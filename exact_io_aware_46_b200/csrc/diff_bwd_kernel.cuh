@@ -18,32 +18,32 @@
 //   dP^T = V dO^T              (SS, 128 columns)
 //   dV  += W^T dO              (TS, W = P_1 - lam P_2 in bf16 over the S columns)
 //   dK_m += dS_m^T Q_m         (SS, N = 64, dS_m staged in shared memory)
-//   dQ_m  = dS_m K_m           (SS, N = 64, lanes = query rows, over the dP columns)
+//   dQ_m^T = K_m^T dS_m^T      (SS, M = 64, lanes = head dimension, over the dP columns:
+//                               map 1 in lanes 0-15 of each 32, map 2 in lanes 16-31)
 // dV (d columns) and dK (64 per map) stay in TMEM for the item: 512 columns in all.
-// At d = 64 the maps are 32 columns wide but the products still run at N = 64
-// over the whole 64-column panel -- with N this small an SS product is bound by
-// reading A -- and the half that belongs to the other map is not read.
+// At d = 64 the maps are 32 columns wide but the products still run over the whole
+// 64-column panel -- with N this small an SS product is bound by reading A, and M has
+// no smaller value -- and the half that belongs to the other map is not read.
 //
 // Warps 0-15 form P, W and dS (a key row per thread, four warps per row with 32
-// query rows each), 16-19 move dQ from TMEM through shared memory into the fp32
-// accumulator by tensor reduce-adds (staged in the dS buffers, which the products
-// have left by then: d = 128 has no shared memory to spare), 20 feeds TMA, 21
-// issues the MMAs.
+// query rows each) and between P_1 and P_2 add the previous tile's dQ^T into the
+// fp32 accumulator, 32 of its columns a warp, with 4-byte reductions that cover 128
+// contiguous bytes (the accumulator's columns are ordered as the lanes are); warp
+// 16 feeds TMA, warp 17 issues the MMAs.  The additions happen at L2, whose rate
+// bounds the kernel at d = 128: 64 KB per tile and SM take 2.1 us whichever way they
+// are sent (measured: reductions of 4 bytes a lane 4628 GB/s, bulk reduce-adds 4593,
+// tensor reduce-adds 4312, 16 bytes a lane with a row per lane 2484), so the way that
+// needs no shared memory was taken: staging dQ in the dS buffers, the only room left,
+// tied each tile's dS to the reduce-adds of the last (2715 us on causal B2 H16 L8192).
 //
 // dlam needs more of P_2 than bf16 gives: its terms P_2 dP have both signs, and
 // the roundings of P_2 (2^-9 relative on average) do not shrink with the sum.
-// P_2 is therefore kept to 16 mantissa bits until dP is there.  Sums per (item, head,
+// P_2 is therefore kept in fp32 until dP is there.  Sums per (item, head,
 // warp) go to the workspace and are added in a fixed order, so dlam is the same
 // from run to run.
 #pragma once
 
 #include "bwd_kernel.cuh"
-
-namespace attn_bwd_impl {
-// fp32 view [heads][Lqp][d] of the dQ accumulator, boxes of 32 columns x 128 rows,
-// 128-byte swizzle (defined with the C entry points)
-bool make_tmap_acc(CUtensorMap* m, float* base, int d, int Lqp, long long heads);
-}  // namespace attn_bwd_impl
 
 namespace attn_diff_bwd_impl {
 
@@ -57,11 +57,10 @@ using attn_bwd_impl::st_global_v8;
 using attn_bwd_impl::tile_of;
 
 constexpr int NSMX = 16;  // P/dS warps: 4 lane quarters x 4 quarters of the query rows
-constexpr int W_DRAIN = NSMX;
-constexpr int W_LOAD = NSMX + 4;
-constexpr int W_MMA = NSMX + 5;
-constexpr int NTHREADS = 32 * (NSMX + 6);
-constexpr int ITEM_READERS = NSMX + 4 + 1;
+constexpr int W_LOAD = NSMX;
+constexpr int W_MMA = NSMX + 1;
+constexpr int NTHREADS = 32 * (NSMX + 2);
+constexpr int ITEM_READERS = NSMX + 1;
 constexpr int NQS = 2;  // Q ring stages
 
 template <int DH>
@@ -82,11 +81,19 @@ struct Cfg {
 };
 constexpr uint32_t IDESC_S = sm100::idesc_bf16_f32(128, BMQ, false, false);
 constexpr uint32_t IDESC_DK = sm100::idesc_bf16_f32(128, 64, false, true);
-constexpr uint32_t IDESC_DQ = sm100::idesc_bf16_f32(128, 64, true, true);
+constexpr uint32_t IDESC_DQ = sm100::idesc_bf16_f32(64, BMQ, true, true);
+
+// Where column c of a dQ row lies in the accumulator's row: the order of the TMEM lanes of
+// dQ^T, so that a warp's 32 lanes add into 128 contiguous bytes (d = 64: the natural order,
+// a half-warp adds 64 bytes).
+template <int DH>
+__host__ __device__ constexpr int acc_pos(int c) {
+  return DH == 128 ? 32 * ((c & 63) >> 4) + 16 * (c >> 6) + (c & 15) : c;
+}
 
 // TMEM columns
 constexpr uint32_t S_COL = 0;     // S_m^T; W^T in the first 16 of each warp's 32 columns
-constexpr uint32_t DP_COL = 128;  // dP^T, then dQ_1 and dQ_2 (64 each)
+constexpr uint32_t DP_COL = 128;  // dP^T, then dQ_1^T and dQ_2^T in alternate 16 lanes
 constexpr uint32_t DV_COL = 256;
 constexpr uint32_t DK_COL = 384;  // dK_1, dK_2 (64 each)
 
@@ -169,7 +176,8 @@ __global__ void __launch_bounds__(256)
     const size_t row = i / (DH / 4);
     const int c4 = static_cast<int>(i % (DH / 4));
     const size_t bh = row / Lq, r = row % Lq;
-    const float4 v = reinterpret_cast<const float4*>(dq_acc + (bh * Lqp + r) * DH)[c4];
+    const float4 v = *reinterpret_cast<const float4*>(dq_acc + (bh * Lqp + r) * DH +
+                                                      acc_pos<DH>(4 * c4));
     uint2 o;
     o.x = sm100::pack_bf16x2(v.x * scale, v.y * scale);
     o.y = sm100::pack_bf16x2(v.z * scale, v.w * scale);
@@ -210,7 +218,7 @@ template <int DH>
 __global__ void __launch_bounds__(NTHREADS, 1)
     main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                const __grid_constant__ CUtensorMap tmAcc, const Params p) {
+                const Params p) {
   using C = Cfg<DH>;
   // the swizzle panels need 1024-byte alignment; at d = 128 there is no room to align by hand
   extern __shared__ __align__(1024) uint8_t smem_diff[];
@@ -236,16 +244,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* w_full = bars + 13;
   uint64_t* dp_full = bars + 14;
   uint64_t* ds_full = bars + 15;
-  uint64_t* ds_free = bars + 16;  // the dS buffers: dQ staged there has left
+  uint64_t* ds_free = bars + 16;   // the dS buffers: every product has read them
   uint64_t* dq_full = bars + 17;
   uint64_t* dq_empty = bars + 18;  // the dP columns: dQ has left
   uint64_t* dkv_full = bars + 19;
   uint64_t* dkv_empty = bars + 20;
   uint64_t* drain = bars + 21;
-  uint64_t* st_full = bars + 22;  // dQ is staged (a bounded wait, unlike a named barrier)
-  uint64_t* item_full = bars + 23;   // [NI]
-  uint64_t* item_empty = bars + 27;  // [NI]
-  int* item_ring = reinterpret_cast<int*>(bars + 31);  // [NI]
+  uint64_t* item_full = bars + 22;   // [NI]
+  uint64_t* item_empty = bars + 26;  // [NI]
+  int* item_ring = reinterpret_cast<int*>(bars + 30);  // [NI]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_ring + NI);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -270,11 +277,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     init(ds_full, NSMX);
     init(ds_free, 1);
     init(dq_full, 1);
-    init(dq_empty, 4);
+    init(dq_empty, NSMX);
     init(dkv_full, 1);
     init(dkv_empty, NSMX);
     init(drain, 1);
-    init(st_full, 4);
     for (int i = 0; i < NI; ++i) {
       init(&item_full[i], 1);
       init(&item_empty[i], ITEM_READERS);
@@ -287,7 +293,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     sm100::prefetch_tmap(&tmdO);
     sm100::prefetch_tmap(&tmK);
     sm100::prefetch_tmap(&tmV);
-    sm100::prefetch_tmap(&tmAcc);
   }
   if (warp == W_MMA) {
     sm100::tmem_alloc(tmem_slot, 512);
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     };
     const uint64_t do_mn = sm100::sdesc_sw128(doA, PANEL, 1024);
-    // dK_m += dS_m^T Q_m and dQ_m = dS_m K_m, eight K steps of 16 each; at d = 64 both
+    // dK_m += dS_m^T Q_m and dQ_m^T = K_m^T dS_m^T, eight K steps of 16 each; at d = 64 both
     // maps multiply the one 64-column panel
     constexpr uint32_t MPANEL = DH == 128 ? PANEL : 0;
     auto issue_dk = [&](uint32_t tile, int m, bool first) {
@@ -414,8 +419,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (leader) {
 #pragma unroll
         for (int k = 0; k < BN / 16; ++k)
-          sm100::mma_ss(tmem + DP_COL + 64 * m, ds_mn + ((k * 2048) >> 4),
-                        k_mn + ((k * 2048) >> 4), IDESC_DQ, k > 0 ? 1u : 0u);
+          sm100::mma_ss(tmem + DP_COL + (static_cast<uint32_t>(16 * m) << 16),
+                        k_mn + ((k * 2048) >> 4), ds_mn + ((k * 2048) >> 4), IDESC_DQ,
+                        k > 0 ? 1u : 0u);
       }
     };
     // K and V rows at and past the sequence's end (kv_len < Lk) may hold anything:
@@ -446,26 +452,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       sm100::tc_fence_after();
       issue_s(tq, 0);
       commit(s1_full);
-      // the products of dS(tile): both dK, both dQ; then its dS, Q and dP columns move on
-      auto issue_ds_products = [&](uint32_t tile, bool first) -> bool {
+      auto issue_both_dq = [&](uint32_t tile) -> bool {
         if (!wait(ds_full, tile & 1, 51)) return false;
         sm100::tc_fence_after();
-        for (int m = 0; m < 2; ++m) {
-          issue_dq(m);
-          issue_dk(tile, m, first);
-        }
+        issue_dq(0);
+        issue_dq(1);
         commit(dq_full);
-        commit(&q_empty[tile % NQS]);
         return true;
       };
+      // Issue order of tile t: dQ(t-1) | S_2(t) | dK_1(t-1) | dP(t) | dK_2(t-1) | dV(t) | S_1(t+1).
+      // P_1(t) forms during dQ(t-1); the softmax warps then take dQ(t-1) out while
+      // S_2(t) and dK_1(t-1) run, so dP(t) finds its columns free; P_2 and W form during
+      // dP(t) and dK_2(t-1).
       for (int t = 0; t < it.T && ok; ++t) {
         const uint32_t cur = tq + t;
         const uint32_t par = cur & 1;
-        if (t > 0 && !(ok = issue_ds_products(cur - 1, t == 1))) break;
+        if (t > 0 && !(ok = issue_both_dq(cur - 1))) break;
         if (!(ok = wait(s1_read, par, 52))) break;
         sm100::tc_fence_after();
         issue_s(cur, 1);
         commit(s2_full);
+        if (t > 0) issue_dk(cur - 1, 0, t == 1);
         if (!(ok = wait(do_full, par, 53))) break;
         if (!(ok = wait(dq_empty, par ^ 1, 54))) break;
         sm100::tc_fence_after();
@@ -481,6 +488,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
         commit(dp_full);
+        if (t > 0) {
+          issue_dk(cur - 1, 1, t == 1);
+          commit(ds_free);
+          commit(&q_empty[(cur - 1) % NQS]);
+        }
         if (!(ok = wait(w_full, par, 55))) break;
         if (t == 0 && !(ok = wait(dkv_empty, (ik & 1) ^ 1, 56))) break;
         sm100::tc_fence_after();
@@ -500,15 +512,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
       if (!ok) break;
-      if (!(ok = issue_ds_products(tq + it.T - 1, it.T == 1))) break;
+      const uint32_t last = tq + it.T - 1;
+      if (!(ok = issue_both_dq(last))) break;
+      issue_dk(last, 0, it.T == 1);
+      issue_dk(last, 1, it.T == 1);
+      commit(ds_free);
+      commit(&q_empty[last % NQS]);
       tq += it.T;
       commit(dkv_full);
       commit(kv_empty);
     }
     commit(drain);
     sm100::mbar_wait_drain(drain, 0);
-  } else if (warp < NSMX) {
-    // ------------------------------------------------------------ P, W and dS
+  } else {
+    // ------------------------------------------------------------ P, W and dS; dQ
     const int qd = warp & 3, cq = warp >> 2;
     const int kl_ = qd * 32 + sm100::lane_id();  // key row within the tile = TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
@@ -520,6 +537,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const float4* d2v = reinterpret_cast<const float4*>(smem + C::OFF_LD + 1536 + cq * 128);
     uint8_t* line = smem + C::OFF_DS + (cq >> 1) * PANEL + kl_ * 128;
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+    // this lane's place in an accumulator row (d = 64: only the half of the lanes whose map owns
+    // this quarter's columns)
+    const int lane = sm100::lane_id();
+    const int acc_lane = DH == 128 ? 32 * qd + lane : 16 * qd + (lane & 15);
+    const bool acc_on = DH == 128 || (lane >> 4) == (qd >> 1);
     uint32_t tq = 0;
     bool ok = true;
     auto arrive = [&](uint64_t* bar) {
@@ -543,6 +565,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (it.T == 0 && sm100::lane_id() == 0)
         for (int g = 0; g < p.G; ++g) lam_part[g * NSMX + warp] = 0.f;
       float2 lam_acc = make_float2(0.f, 0.f);
+      // adds this warp's 32 rows of a tile's dQ^T (lanes = head dimension) into the accumulator
+      auto drain_dq = [&](int t) -> bool {
+        int g, i;
+        tile_of(it, t, nq, g, i);
+        const size_t row = static_cast<size_t>(it.b * p.Hq + it.hkv * p.G + g) * p.Lqp +
+                           i * BMQ + 32 * cq;
+        float* acc = p.dq_acc + row * DH + acc_lane;
+        if (!wait(dq_full, (tq + t) & 1, 65)) return false;
+        sm100::tc_fence_after();
+        uint32_t v[32];
+        sm100::tmem_ld32(dp_addr, v);
+        sm100::tmem_ld_wait();
+        arrive(dq_empty);
+        if (acc_on) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) attn_bwd_impl::red_add_f32(acc + c * DH, __uint_as_float(v[c]));
+        }
+        return true;
+      };
       for (int t = 0; t < it.T && ok; ++t) {
         const uint32_t par = (tq + t) & 1;
         int g, i;
@@ -588,30 +629,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           p1[2 * c4] = sm100::pack_bf16x2(e0.x, e0.y);
           p1[2 * c4 + 1] = sm100::pack_bf16x2(e1.x, e1.y);
         }
-        // ---- P_2, kept to 16 mantissa bits (upper halves of pairs, next bytes of fours),
-        // and W = P_1 - lam P_2
+        // ---- the previous tile's dQ
+        if (t > 0 && !(ok = drain_dq(t - 1))) break;
+        // ---- P_2, kept in fp32, and W = P_1 - lam P_2
         if (!(ok = wait(s2_full, par, 60))) break;
         sm100::tc_fence_after();
         load_s();
         mask_s();
-        uint32_t hi[16], lo[8];
+        float2 p2[16];
+        uint32_t wv[16];
 #pragma unroll
         for (int c4 = 0; c4 < 8; ++c4) {
           const float4 nl = l2v[c4];
-          const float2 e0 = prob(2 * c4, make_float2(nl.x, nl.y));
-          const float2 e1 = prob(2 * c4 + 1, make_float2(nl.z, nl.w));
-          const uint32_t a = __float_as_uint(e0.x), b = __float_as_uint(e0.y);
-          const uint32_t c = __float_as_uint(e1.x), d = __float_as_uint(e1.y);
-          hi[2 * c4] = __byte_perm(a, b, 0x7632);
-          hi[2 * c4 + 1] = __byte_perm(c, d, 0x7632);
-          lo[c4] = __byte_perm(__byte_perm(a, b, 0x0051), __byte_perm(c, d, 0x0051), 0x5410);
-          const uint32_t u0 = p1[2 * c4], u1 = p1[2 * c4 + 1];
-          const float2 w0 = __ffma2_rn(e0, nlam, f2(u0 << 16, u0 & 0xFFFF0000u));
-          const float2 w1 = __ffma2_rn(e1, nlam, f2(u1 << 16, u1 & 0xFFFF0000u));
-          s[2 * c4] = sm100::pack_bf16x2(w0.x, w0.y);
-          s[2 * c4 + 1] = sm100::pack_bf16x2(w1.x, w1.y);
+          p2[2 * c4] = prob(2 * c4, make_float2(nl.x, nl.y));
+          p2[2 * c4 + 1] = prob(2 * c4 + 1, make_float2(nl.z, nl.w));
+#pragma unroll
+          for (int e = 2 * c4; e < 2 * c4 + 2; ++e) {
+            const float2 w =
+                __ffma2_rn(p2[e], nlam, f2(p1[e] << 16, p1[e] & 0xFFFF0000u));
+            wv[e] = sm100::pack_bf16x2(w.x, w.y);
+          }
         }
-        sm100::tmem_st16(s_addr, s);
+        sm100::tmem_st16(s_addr, wv);
         sm100::tmem_st_wait();
         arrive(w_full);
         // ---- dS_1 = P_1 (dP - D_1), dS_2 = P_2 (-lam dP + lam D_2): row-contiguous per key,
@@ -625,38 +664,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           uint32_t dp[16];
           sm100::tmem_ld16(dp_addr + 16 * h, dp);
           sm100::tmem_ld_wait();
-          uint32_t w1[8], w2[8];
 #pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
-            const int cc = 4 * h + c4;  // columns 4 cc ... of the thread's 32
-            const float4 n1 = d1v[cc], n2 = d2v[cc];
-            const float2 g0 = f2(dp[4 * c4], dp[4 * c4 + 1]);
-            const float2 g1 = f2(dp[4 * c4 + 2], dp[4 * c4 + 3]);
-            const uint32_t u0 = p1[2 * cc], u1 = p1[2 * cc + 1];
-            const float2 a0 = __fmul2_rn(f2(u0 << 16, u0 & 0xFFFF0000u),
-                                         __fadd2_rn(g0, make_float2(n1.x, n1.y)));
-            const float2 a1 = __fmul2_rn(f2(u1 << 16, u1 & 0xFFFF0000u),
-                                         __fadd2_rn(g1, make_float2(n1.z, n1.w)));
-            const float2 q0 = f2(__byte_perm(hi[2 * cc], lo[cc], 0x1044),
-                                 __byte_perm(hi[2 * cc], lo[cc], 0x3255));
-            const float2 q1 = f2(__byte_perm(hi[2 * cc + 1], lo[cc], 0x1066),
-                                 __byte_perm(hi[2 * cc + 1], lo[cc], 0x3277));
-            lam_acc = __ffma2_rn(q0, g0, lam_acc);
-            lam_acc = __ffma2_rn(q1, g1, lam_acc);
-            const float2 b0 = __fmul2_rn(q0, __ffma2_rn(g0, nlam, make_float2(n2.x, n2.y)));
-            const float2 b1 = __fmul2_rn(q1, __ffma2_rn(g1, nlam, make_float2(n2.z, n2.w)));
-            w1[2 * c4] = sm100::pack_bf16x2(a0.x, a0.y);
-            w1[2 * c4 + 1] = sm100::pack_bf16x2(a1.x, a1.y);
-            w2[2 * c4] = sm100::pack_bf16x2(b0.x, b0.y);
-            w2[2 * c4 + 1] = sm100::pack_bf16x2(b1.x, b1.y);
-          }
+          for (int q = 0; q < 2; ++q) {  // eight columns: one 16-byte chunk of each map
+            uint32_t w1[4], w2[4];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+            for (int k = 0; k < 2; ++k) {
+              const int cc = 4 * h + 2 * q + k;  // columns 4 cc ... of the thread's 32
+              const float4 n1 = d1v[cc], n2 = d2v[cc];
+              const float2 nd1[2] = {make_float2(n1.x, n1.y), make_float2(n1.z, n1.w)};
+              const float2 ld2[2] = {make_float2(n2.x, n2.y), make_float2(n2.z, n2.w)};
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int cp = 2 * cc + e;
+                const float2 gp = f2(dp[8 * q + 4 * k + 2 * e], dp[8 * q + 4 * k + 2 * e + 1]);
+                const float2 a =
+                    __fmul2_rn(f2(p1[cp] << 16, p1[cp] & 0xFFFF0000u), __fadd2_rn(gp, nd1[e]));
+                const float2 b = __fmul2_rn(p2[cp], __ffma2_rn(gp, nlam, ld2[e]));
+                lam_acc = __ffma2_rn(p2[cp], gp, lam_acc);
+                w1[2 * k + e] = sm100::pack_bf16x2(a.x, a.y);
+                w2[2 * k + e] = sm100::pack_bf16x2(b.x, b.y);
+              }
+            }
             uint8_t* at = line + (((4 * (cq & 1) + 2 * h + q) ^ (kl_ & 7)) << 4);
-            *reinterpret_cast<uint4*>(at) =
-                make_uint4(w1[4 * q], w1[4 * q + 1], w1[4 * q + 2], w1[4 * q + 3]);
-            *reinterpret_cast<uint4*>(at + 2 * PANEL) =
-                make_uint4(w2[4 * q], w2[4 * q + 1], w2[4 * q + 2], w2[4 * q + 3]);
+            *reinterpret_cast<uint4*>(at) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+            *reinterpret_cast<uint4*>(at + 2 * PANEL) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
           }
         }
         sm100::fence_proxy_async_smem();
@@ -670,6 +701,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
       if (!ok) break;
+      if (it.T > 0 && !(ok = drain_dq(it.T - 1))) break;
       tq += it.T;
       // ---------------- epilogue: dV, dK (x scale) of this key row, a quarter of the columns
       if (!(ok = wait(dkv_full, ik & 1, 64))) break;
@@ -708,61 +740,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       arrive(dkv_empty);
     }
-  } else {
-    // ------------------------------------------------------------ dQ drain
-    // dQ_m (lanes = the tile's rows) through the dS buffer of its map, which every
-    // product has read: boxes of 128 rows x 32 columns in the 128-byte swizzle of the
-    // accumulator's tensor map, added by tensor reduce-adds
-    const int tid = threadIdx.x - 32 * W_DRAIN;  // = TMEM lane
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    uint32_t tq = 0;
-    bool ok = true;
-    for (uint32_t ik = 0; ok; ++ik) {
-      int w;
-      if (!(ok = next_item(ik, w)) || w < 0) break;
-      const Item it = get_item(p, w, nullptr);
-      const int nq = it.T > 0 ? it.T / p.G : 0;
-      for (int t = 0; t < it.T && ok; ++t) {
-        const uint32_t cur = tq + t;
-        int g, i;
-        tile_of(it, t, nq, g, i);
-        const int qh = it.b * p.Hq + it.hkv * p.G + g;
-        if (!(ok = wait(dq_full, cur & 1, 65))) break;
-        sm100::tc_fence_after();
-        constexpr int BOXES = DH / 32;  // of both maps: box b is columns 32 b ...
-#pragma unroll
-        for (int b = 0; b < BOXES; ++b) {
-          uint32_t v[32];
-          // d = 64: map b's own 32 columns of its full-width product
-          sm100::tmem_ld32(tmem + lane_base + DP_COL + (DH == 64 ? 96 * b : 32 * b), v);
-          sm100::tmem_ld_wait();
-          uint8_t* box = smem + C::OFF_DS + b * (BMQ * 128) + tid * 128;
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(box + ((c ^ (tid & 7)) << 4)) =
-                make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-        }
-        sm100::fence_proxy_async_smem();
-        sm100::tc_fence_before();
-        __syncwarp();
-        if (sm100::lane_id() == 0) {
-          sm100::mbar_arrive(dq_empty);
-          sm100::mbar_arrive(st_full);
-        }
-        if (tid == 0) {
-          if (!(ok = wait(st_full, cur & 1, 66))) break;
-          for (int b = 0; b < BOXES; ++b)
-            attn_bwd_impl::tma_reduce_add_3d(&tmAcc, smem + C::OFF_DS + b * (BMQ * 128), 32 * b,
-                                             i * BMQ, qh);
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          attn_bwd_impl::bulk_wait_read_all();
-          sm100::mbar_arrive(ds_free);
-        }
-      }
-      tq += it.T;
-    }
-    // the finishing pass reads the accumulator after this kernel
-    if (tid == 0) attn_bwd_impl::bulk_wait_all();
   }
 
   sm100::tc_fence_before();
@@ -849,12 +826,11 @@ attn_status_t launch_d(const Args& a, cudaStream_t s) {
     const void* q = a.Lq > 0 ? a.Q : a.K;
     const void* g = a.Lq > 0 ? a.dO : a.K;
     const long long kvh = static_cast<long long>(a.B) * a.Hkv;
-    CUtensorMap tq, tdo, tk, tv, tacc;
+    CUtensorMap tq, tdo, tk, tv;
     if (!attn_bwd_impl::make_tmap_rows(&tq, q, DH, a.Lq, BH, BMQ) ||
         !attn_bwd_impl::make_tmap_rows(&tdo, g, DH, a.Lq, BH, BMQ) ||
         !attn_bwd_impl::make_tmap_rows(&tk, a.K, DH, a.Lk, kvh, BN) ||
-        !attn_bwd_impl::make_tmap_rows(&tv, a.V, DH, a.Lk, kvh, BN) ||
-        !attn_bwd_impl::make_tmap_acc(&tacc, p.dq_acc, DH, p.Lqp, BH)) {
+        !attn_bwd_impl::make_tmap_rows(&tv, a.V, DH, a.Lk, kvh, BN)) {
       attn_host::report(cudaErrorInvalidValue, "diff bwd tensor maps");
       return ATTN_ERR_CUDA;
     }
@@ -862,7 +838,7 @@ attn_status_t launch_d(const Args& a, cudaStream_t s) {
                           "diff main_kernel shared-memory attribute") != cudaSuccess)
       return ATTN_ERR_CUDA;
     const int grid = p.n_items < a.sms ? p.n_items : a.sms;
-    main_kernel<DH><<<grid, NTHREADS, C::SMEM_BYTES, s>>>(tq, tdo, tk, tv, tacc, p);
+    main_kernel<DH><<<grid, NTHREADS, C::SMEM_BYTES, s>>>(tq, tdo, tk, tv, p);
     if (attn_host::report_launch(main_kernel<DH>, "diff main_kernel") != cudaSuccess)
       return ATTN_ERR_CUDA;
   }
