@@ -59,8 +59,9 @@ using attn_bwd_impl::tile_of;
 constexpr int NSMX = 16;  // P/dS warps: 4 lane quarters x 4 quarters of the query rows
 constexpr int W_LOAD = NSMX;
 constexpr int W_MMA = NSMX + 1;
-constexpr int NTHREADS = 32 * (NSMX + 2);
-constexpr int ITEM_READERS = NSMX + 1;
+constexpr int W_HALF = NSMX + 2;  // two warps: each half's statistics and dO
+constexpr int NTHREADS = 32 * (NSMX + 4);
+constexpr int ITEM_READERS = NSMX + 3;
 constexpr int NQS = 2;  // Q ring stages
 
 template <int DH>
@@ -73,15 +74,17 @@ struct Cfg {
   static constexpr int OFF_Q = 2 * TILE;             // NQS stages
   static constexpr int OFF_DO = OFF_Q + NQS * TILE;
   static constexpr int OFF_DS = OFF_DO + TILE;       // dS_1^T, dS_2^T: two panels of 64 rows each
-  static constexpr int OFF_LD = OFF_DS + 4 * PANEL;  // -lse2_1, -lse2_2, -D_1, lam D_2: [128] each
+  static constexpr int OFF_LD = OFF_DS + 4 * PANEL;  // [half] -lse2_1, -lse2_2, -D_1, lam D_2: [64]
   static constexpr int OFF_BAR = OFF_LD + 2048;
   static constexpr int SMEM_BYTES = OFF_BAR + 512;
   static_assert(SMEM_BYTES <= 232448, "dynamic shared memory limit");
   static constexpr uint32_t IDESC_DV = sm100::idesc_bf16_f32(128, DH, false, true);
 };
-constexpr uint32_t IDESC_S = sm100::idesc_bf16_f32(128, BMQ, false, false);
+constexpr int HQ = 64;             // query rows of a half tile, the unit of each warp group
+constexpr int HROWS = HQ * 128;    // bytes of 64 rows of a swizzle panel
+constexpr uint32_t IDESC_S = sm100::idesc_bf16_f32(128, HQ, false, false);
 constexpr uint32_t IDESC_DK = sm100::idesc_bf16_f32(128, 64, false, true);
-constexpr uint32_t IDESC_DQ = sm100::idesc_bf16_f32(64, BMQ, true, true);
+constexpr uint32_t IDESC_DQ = sm100::idesc_bf16_f32(64, HQ, true, true);
 
 // Where column c of a dQ row lies in the accumulator's row: the order of the TMEM lanes of
 // dQ^T, so that a warp's 32 lanes add into 128 contiguous bytes (d = 64: the natural order,
@@ -98,10 +101,10 @@ constexpr uint32_t DV_COL = 256;
 constexpr uint32_t DK_COL = 384;  // dK_1, dK_2 (64 each)
 
 // Column pairs cp of a 16-pair block with (cp & 7) >= POLY_FROM take the FMA-pipe exp2.
-constexpr int POLY_FROM = 6;
+constexpr int POLY_FROM = 8;
 
 struct Params : attn_bwd_impl::Params {
-  const float* stats;  // [B*Hq][n_qt][4][128]: -lse2_1, -lse2_2, -D_1, lam D_2
+  const float* stats;  // [B*Hq][n_qt][2 halves][4][64]: -lse2_1, -lse2_2, -D_1, lam D_2
   const float* lam;    // [n_lam]
   int n_lam;
   float* lam_part;  // [n_items][G][NSMX] sums of P_2 dP
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(256)
     } else {
       v = lane == 2 ? -(a1 + l * a2) : l * a2;
     }
-    stats[(static_cast<size_t>(bh) * (Lqp / BMQ) + r / BMQ) * 512 + lane * 128 + r % BMQ] = v;
+    stats[(static_cast<size_t>(bh) * (Lqp / HQ) + r / HQ) * 256 + lane * HQ + r % HQ] = v;
   }
 }
 
@@ -232,58 +235,63 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* kv_full = bars + 0;
   uint64_t* kv_empty = bars + 1;
-  uint64_t* q_full = bars + 2;   // [NQS]
-  uint64_t* q_empty = bars + 4;  // [NQS]
-  uint64_t* do_full = bars + 6;
-  uint64_t* do_empty = bars + 7;
-  uint64_t* l_full = bars + 8;    // both -lse2 (free again once W is out)
-  uint64_t* d_full = bars + 9;    // -D_1, lam D_2 (free again once dS is out)
-  uint64_t* s1_full = bars + 10;
-  uint64_t* s1_read = bars + 11;
-  uint64_t* s2_full = bars + 12;
-  uint64_t* w_full = bars + 13;
-  uint64_t* dp_full = bars + 14;
-  uint64_t* ds_full = bars + 15;
-  uint64_t* ds_free = bars + 16;   // the dS buffers: every product has read them
-  uint64_t* dq_full = bars + 17;
-  uint64_t* dq_empty = bars + 18;  // the dP columns: dQ has left
-  uint64_t* dkv_full = bars + 19;
-  uint64_t* dkv_empty = bars + 20;
-  uint64_t* drain = bars + 21;
-  uint64_t* item_full = bars + 22;   // [NI]
-  uint64_t* item_empty = bars + 26;  // [NI]
-  int* item_ring = reinterpret_cast<int*>(bars + 30);  // [NI]
+  uint64_t* dkv_full = bars + 2;
+  uint64_t* dkv_empty = bars + 3;
+  uint64_t* drain = bars + 4;
+  uint64_t* item_full = bars + 5;   // [NI]
+  uint64_t* item_empty = bars + 9;  // [NI]
+  // of each half tile's pipeline h
+  auto half_bar = [&](int h, int i) -> uint64_t* { return bars + 13 + 17 * h + i; };
+  auto q_full = [&](int h, uint32_t tile) { return half_bar(h, tile % NQS); };
+  auto q_empty = [&](int h, uint32_t tile) { return half_bar(h, 2 + tile % NQS); };
+  auto do_full = [&](int h) { return half_bar(h, 4); };
+  auto do_empty = [&](int h) { return half_bar(h, 5); };
+  auto l_full = [&](int h) { return half_bar(h, 6); };  // both -lse2 (free again once W is out)
+  auto d_full = [&](int h) { return half_bar(h, 7); };  // -D_1, lam D_2 (free once dS is out)
+  auto s1_full = [&](int h) { return half_bar(h, 8); };
+  auto s1_read = [&](int h) { return half_bar(h, 9); };
+  auto s2_full = [&](int h) { return half_bar(h, 10); };
+  auto w_full = [&](int h) { return half_bar(h, 11); };
+  auto dp_full = [&](int h) { return half_bar(h, 12); };
+  auto ds_full = [&](int h) { return half_bar(h, 13); };
+  auto ds_free = [&](int h) { return half_bar(h, 14); };  // every product has read dS
+  auto dq_full = [&](int h) { return half_bar(h, 15); };
+  auto dq_empty = [&](int h) { return half_bar(h, 16); };  // the dP columns: dQ has left
+  int* item_ring = reinterpret_cast<int*>(bars + 47);  // [NI]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_ring + NI);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert(47 * 8 + NI * 4 + 8 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     auto init = [](uint64_t* b, uint32_t n) { sm100::mbar_init(b, n); };
     init(kv_full, 1);
     init(kv_empty, 1);
-    for (int s = 0; s < NQS; ++s) {
-      init(&q_full[s], 1);
-      init(&q_empty[s], 1);
-    }
-    init(do_full, 1);
-    init(do_empty, 1);
-    init(l_full, 1);
-    init(d_full, 1);
-    init(s1_full, 1);
-    init(s1_read, NSMX);
-    init(s2_full, 1);
-    init(w_full, NSMX);
-    init(dp_full, 1);
-    init(ds_full, NSMX);
-    init(ds_free, 1);
-    init(dq_full, 1);
-    init(dq_empty, NSMX);
     init(dkv_full, 1);
     init(dkv_empty, NSMX);
     init(drain, 1);
     for (int i = 0; i < NI; ++i) {
       init(&item_full[i], 1);
       init(&item_empty[i], ITEM_READERS);
+    }
+    for (int h = 0; h < 2; ++h) {
+      for (uint32_t i = 0; i < NQS; ++i) {
+        init(q_full(h, i), 1);
+        init(q_empty(h, i), 1);
+      }
+      init(do_full(h), 1);
+      init(do_empty(h), 1);
+      init(l_full(h), 1);
+      init(d_full(h), 1);
+      init(s1_full(h), 1);
+      init(s1_read(h), NSMX / 2);
+      init(s2_full(h), 1);
+      init(w_full(h), NSMX / 2);
+      init(dp_full(h), 1);
+      init(ds_full(h), NSMX / 2);
+      init(ds_free(h), 1);
+      init(dq_full(h), 1);
+      init(dq_empty(h), NSMX / 2);
     }
     *abort_flag = 0;
     sm100::fence_barrier_init();
@@ -316,11 +324,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   if (warp == W_LOAD) {
     // ------------------------------------------------------------ TMA producer
-    // per query tile: Q into the two-stage ring, then the tile's statistics, dO and D,
-    // each into a single buffer that the tile before has left by then
+    // the items, K and V of each, and Q of each query tile (a two-stage ring per half)
     if (sm100::lane_id() == 0) {
-      uint32_t tq = 0, ik = 0, kv_issued = 0;
-      int last_q[NQS] = {-1, -1}, last_l = -1, last_do = -1, last_d = -1;
+      uint32_t tq = 0, ik = 0, kv_issued = 0, n_q[2] = {0, 0};
       bool ok = true;
       for (; ok; ++ik) {
         if (!(ok = wait(&item_empty[ik % NI], ((ik / NI) & 1) ^ 1, 42))) break;
@@ -343,38 +349,65 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int t = 0; t < it.T && ok; ++t, ++tq) {
           int g, i;
           tile_of(it, t, nq, g, i);
-          const int slot = tq % NQS;
-          const int qh = it.b * p.Hq + it.hkv * p.G + g;
-          const float* st = p.stats + (static_cast<size_t>(qh) * p.n_qt + i) * 512;
-          if (!(ok = wait(&q_empty[slot], ((tq / NQS) & 1) ^ 1, 44))) break;
-          sm100::mbar_arrive_expect_tx(&q_full[slot], C::TILE);
-          for (int c = 0; c < C::PANELS; ++c)
-            sm100::tma_load_3d(&tmQ, &q_full[slot], smem + C::OFF_Q + slot * C::TILE + c * PANEL,
-                               c * 64, i * BMQ, qh);
-          last_q[slot] = static_cast<int>(tq);
-          if (!(ok = wait(w_full, (tq & 1) ^ 1, 45))) break;
-          sm100::mbar_arrive_expect_tx(l_full, 1024);
-          attn_bwd_impl::bulk_g2s(smem + C::OFF_LD, st, 1024, l_full);
-          last_l = static_cast<int>(tq);
-          if (!(ok = wait(do_empty, (tq & 1) ^ 1, 46))) break;
-          sm100::mbar_arrive_expect_tx(do_full, C::TILE);
-          for (int c = 0; c < C::PANELS; ++c)
-            sm100::tma_load_3d(&tmdO, do_full, smem + C::OFF_DO + c * PANEL, c * 64, i * BMQ, qh);
-          last_do = static_cast<int>(tq);
-          if (!(ok = wait(ds_full, (tq & 1) ^ 1, 47))) break;
-          sm100::mbar_arrive_expect_tx(d_full, 1024);
-          attn_bwd_impl::bulk_g2s(smem + C::OFF_LD + 1024, st + 256, 1024, d_full);
-          last_d = static_cast<int>(tq);
+          for (int h = 0; h < 2; ++h) {
+            if (!(ok = wait(q_empty(h, tq), ((tq / NQS) & 1) ^ 1, 44))) break;
+            sm100::mbar_arrive_expect_tx(q_full(h, tq), C::TILE / 2);
+            for (int c = 0; c < C::PANELS; ++c)
+              sm100::tma_load_3d(&tmQ, q_full(h, tq),
+                                 smem + C::OFF_Q + (tq % NQS) * C::TILE + c * PANEL + h * HROWS,
+                                 c * 64, i * BMQ + h * HQ, it.b * p.Hq + it.hkv * p.G + g);
+            ++n_q[h];
+          }
         }
       }
       // the CTA must not exit while copies still land in its shared memory, which an
       // expired wait elsewhere could otherwise allow
       if (kv_issued > 0) sm100::mbar_wait_drain(kv_full, (kv_issued - 1) & 1);
-      for (int sl = 0; sl < NQS; ++sl)
-        if (last_q[sl] >= 0) sm100::mbar_wait_drain(&q_full[sl], (last_q[sl] / NQS) & 1);
-      if (last_l >= 0) sm100::mbar_wait_drain(l_full, last_l & 1);
-      if (last_do >= 0) sm100::mbar_wait_drain(do_full, last_do & 1);
-      if (last_d >= 0) sm100::mbar_wait_drain(d_full, last_d & 1);
+      for (int h = 0; h < 2; ++h)
+        for (uint32_t k = n_q[h] > NQS ? n_q[h] - NQS : 0; k < n_q[h]; ++k)
+          sm100::mbar_wait_drain(q_full(h, k), (k / NQS) & 1);
+    }
+  } else if (warp >= W_HALF) {
+    // ------------------------------------------------------------ a half's statistics and dO
+    // each into a single buffer that the half's tile before has left by then
+    const int h = warp - W_HALF;
+    uint8_t* ld = smem + C::OFF_LD + h * 1024;
+    uint32_t tq = 0, n_l = 0, n_do = 0, n_d = 0;
+    bool ok = true;
+    for (uint32_t ik = 0; ok; ++ik) {
+      int w;
+      if (!(ok = next_item(ik, w)) || w < 0) break;
+      if (sm100::lane_id() == 0) {
+        const Item it = get_item(p, w, nullptr);
+        const int nq = it.T > 0 ? it.T / p.G : 0;
+        for (int t = 0; t < it.T && ok; ++t, ++tq) {
+          int g, i;
+          tile_of(it, t, nq, g, i);
+          const int qh = it.b * p.Hq + it.hkv * p.G + g;
+          const uint32_t par = (tq & 1) ^ 1;
+          const float* st = p.stats + (static_cast<size_t>(qh) * p.n_qt + i) * 512 + h * 256;
+          if (!(ok = wait(w_full(h), par, 45))) break;
+          sm100::mbar_arrive_expect_tx(l_full(h), 512);
+          attn_bwd_impl::bulk_g2s(ld, st, 512, l_full(h));
+          ++n_l;
+          if (!(ok = wait(do_empty(h), par, 46))) break;
+          sm100::mbar_arrive_expect_tx(do_full(h), C::TILE / 2);
+          for (int c = 0; c < C::PANELS; ++c)
+            sm100::tma_load_3d(&tmdO, do_full(h), smem + C::OFF_DO + c * PANEL + h * HROWS, c * 64,
+                               i * BMQ + h * HQ, qh);
+          ++n_do;
+          if (!(ok = wait(ds_full(h), par, 47))) break;
+          sm100::mbar_arrive_expect_tx(d_full(h), 512);
+          attn_bwd_impl::bulk_g2s(ld + 512, st + 128, 512, d_full(h));
+          ++n_d;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (sm100::lane_id() == 0) {
+      if (n_l > 0) sm100::mbar_wait_drain(l_full(h), (n_l - 1) & 1);
+      if (n_do > 0) sm100::mbar_wait_drain(do_full(h), (n_do - 1) & 1);
+      if (n_d > 0) sm100::mbar_wait_drain(d_full(h), (n_d - 1) & 1);
     }
   } else if (warp == W_MMA) {
     // ------------------------------------------------------------ MMA issuer
@@ -387,40 +420,60 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (leader) sm100::tc_commit(bar);
       __syncwarp();
     };
-    // S_m^T: both operands K-major, map m's half of the columns (its own panel at
+    // S_m^T of half h: both operands K-major, map m's half of the columns (its own panel at
     // d = 128, 64 bytes into the rows at d = 64)
-    constexpr uint32_t HALF = DH == 128 ? PANEL : 64;
-    auto issue_s = [&](uint32_t tile, int m) {
-      const uint64_t ad = sm100::sdesc_sw128(kA + m * HALF, 16, 1024);
-      const uint64_t bd = sm100::sdesc_sw128(qA(tile) + m * HALF, 16, 1024);
+    constexpr uint32_t MHALF = DH == 128 ? PANEL : 64;
+    auto issue_s = [&](uint32_t tile, int h, int m) {
+      const uint64_t ad = sm100::sdesc_sw128(kA + m * MHALF, 16, 1024);
+      const uint64_t bd = sm100::sdesc_sw128(qA(tile) + m * MHALF + h * HROWS, 16, 1024);
       if (leader) {
 #pragma unroll
         for (int k = 0; k < DH / 32; ++k)
-          sm100::mma_ss(tmem + S_COL, ad + 2 * k, bd + 2 * k, IDESC_S, k > 0);
+          sm100::mma_ss(tmem + S_COL + HQ * h, ad + 2 * k, bd + 2 * k, IDESC_S, k > 0);
       }
     };
-    const uint64_t do_mn = sm100::sdesc_sw128(doA, PANEL, 1024);
-    // dK_m += dS_m^T Q_m and dQ_m^T = K_m^T dS_m^T, eight K steps of 16 each; at d = 64 both
-    // maps multiply the one 64-column panel
-    constexpr uint32_t MPANEL = DH == 128 ? PANEL : 0;
-    auto issue_dk = [&](uint32_t tile, int m, bool first) {
-      const uint64_t ds_k = sm100::sdesc_sw128(sbase + C::OFF_DS + m * 2 * PANEL, 16, 1024);
-      const uint64_t q_mn = sm100::sdesc_sw128(qA(tile) + m * MPANEL, PANEL, 1024);
+    auto issue_dp = [&](int h) {  // dP^T = V dO^T
+      const uint64_t ad = sm100::sdesc_sw128(vA, 16, 1024);
+      const uint64_t bd = sm100::sdesc_sw128(doA + h * HROWS, 16, 1024);
       if (leader) {
 #pragma unroll
-        for (int k = 0; k < BMQ / 16; ++k)
-          sm100::mma_ss(tmem + DK_COL + 64 * m, ds_k + ((((k >> 2) * PANEL) + (k & 3) * 32) >> 4),
-                        q_mn + ((k * 2048) >> 4), IDESC_DK, (!first || k > 0) ? 1u : 0u);
+        for (int k = 0; k < DH / 16; ++k) {
+          const uint64_t o = static_cast<uint64_t>(((k >> 2) * PANEL + (k & 3) * 32) >> 4);
+          sm100::mma_ss(tmem + DP_COL + HQ * h, ad + o, bd + o, IDESC_S, k > 0);
+        }
       }
     };
-    auto issue_dq = [&](int m) {
-      const uint64_t ds_mn = sm100::sdesc_sw128(sbase + C::OFF_DS + m * 2 * PANEL, PANEL, 1024);
-      const uint64_t k_mn = sm100::sdesc_sw128(kA + m * MPANEL, PANEL, 1024);
+    auto issue_dv = [&](int h, bool first) {  // W: a warp's 32 rows are 16 columns
+      const uint64_t bd = sm100::sdesc_sw128(doA + h * HROWS, PANEL, 1024);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < HQ / 16; ++k)
+          sm100::mma_ts(tmem + DV_COL, tmem + S_COL + HQ * h + (k >> 1) * 32 + (k & 1) * 8,
+                        bd + ((k * 2048) >> 4), C::IDESC_DV, (!first || k > 0) ? 1u : 0u);
+      }
+    };
+    // dK_m += dS_m^T Q_m (K steps of 16 rows) and dQ_m^T = K_m^T dS_m^T (of 16 keys); at d = 64
+    // both maps multiply the one 64-column panel
+    constexpr uint32_t MPANEL = DH == 128 ? PANEL : 0;
+    auto ds_at = [&](int h, int m) { return sbase + C::OFF_DS + (m * 2 + h) * PANEL; };
+    auto issue_dk = [&](uint32_t tile, int h, int m, bool first) {
+      const uint64_t ad = sm100::sdesc_sw128(ds_at(h, m), 16, 1024);
+      const uint64_t bd = sm100::sdesc_sw128(qA(tile) + m * MPANEL + h * HROWS, PANEL, 1024);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < HQ / 16; ++k)
+          sm100::mma_ss(tmem + DK_COL + 64 * m, ad + 2 * k, bd + ((k * 2048) >> 4), IDESC_DK,
+                        (!first || k > 0) ? 1u : 0u);
+      }
+    };
+    auto issue_dq = [&](int h, int m) {
+      const uint64_t bd = sm100::sdesc_sw128(ds_at(h, m), PANEL, 1024);
+      const uint64_t ad = sm100::sdesc_sw128(kA + m * MPANEL, PANEL, 1024);
       if (leader) {
 #pragma unroll
         for (int k = 0; k < BN / 16; ++k)
-          sm100::mma_ss(tmem + DP_COL + (static_cast<uint32_t>(16 * m) << 16),
-                        k_mn + ((k * 2048) >> 4), ds_mn + ((k * 2048) >> 4), IDESC_DQ,
+          sm100::mma_ss(tmem + DP_COL + HQ * h + (static_cast<uint32_t>(16 * m) << 16),
+                        ad + ((k * 2048) >> 4), bd + ((k * 2048) >> 4), IDESC_DQ,
                         k > 0 ? 1u : 0u);
       }
     };
@@ -448,76 +501,77 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         continue;
       }
       if (it.kv_len < p.Lk && it.kv_len < (it.n + 1) * BN) clear_tail(it.kv_len - it.n * BN);
-      if (!(ok = wait(&q_full[tq % NQS], (tq / NQS) & 1, 50))) break;
-      sm100::tc_fence_after();
-      issue_s(tq, 0);
-      commit(s1_full);
-      auto issue_both_dq = [&](uint32_t tile) -> bool {
-        if (!wait(ds_full, tile & 1, 51)) return false;
+      // the first product of a half's tile, as soon as its Q is there (its S columns are free:
+      // the half's dV before has been issued)
+      auto first_s = [&](uint32_t tile, int h) -> bool {
+        if (!wait(q_full(h, tile), (tile / NQS) & 1, 50)) return false;
         sm100::tc_fence_after();
-        issue_dq(0);
-        issue_dq(1);
-        commit(dq_full);
+        issue_s(tile, h, 0);
+        commit(s1_full(h));
         return true;
       };
-      // Issue order of tile t: dQ(t-1) | S_2(t) | dK_1(t-1) | dP(t) | dK_2(t-1) | dV(t) | S_1(t+1).
-      // P_1(t) forms during dQ(t-1); the softmax warps then take dQ(t-1) out while
-      // S_2(t) and dK_1(t-1) run, so dP(t) finds its columns free; P_2 and W form during
-      // dP(t) and dK_2(t-1).
+      auto both_dq = [&](uint32_t tile, int h) -> bool {
+        if (!wait(ds_full(h), tile & 1, 51)) return false;
+        sm100::tc_fence_after();
+        issue_dq(h, 0);
+        issue_dq(h, 1);
+        commit(dq_full(h));
+        return true;
+      };
+      // S_2 of the half's tile t, with the first dK of its tile t - 1 behind it
+      auto second_s = [&](int t, int h) -> bool {
+        const uint32_t cur = tq + t;
+        if (!wait(s1_read(h), cur & 1, 52)) return false;
+        sm100::tc_fence_after();
+        issue_s(cur, h, 1);
+        commit(s2_full(h));
+        if (t > 0) issue_dk(cur - 1, h, 0, t == 1 && h == 0);
+        return true;
+      };
+      auto second_dk = [&](uint32_t tile, int h, bool first) {
+        issue_dk(tile, h, 1, first);
+        commit(ds_free(h));
+        commit(q_empty(h, tile));
+      };
+      auto dp_dk = [&](int t, int h) -> bool {
+        const uint32_t cur = tq + t;
+        if (!wait(do_full(h), cur & 1, 53)) return false;
+        if (!wait(dq_empty(h), (cur & 1) ^ 1, 54)) return false;
+        sm100::tc_fence_after();
+        issue_dp(h);
+        commit(dp_full(h));
+        if (t > 0) second_dk(cur - 1, h, t == 1 && h == 0);
+        return true;
+      };
+      auto dv_s = [&](int t, int h) -> bool {
+        const uint32_t cur = tq + t;
+        if (!wait(w_full(h), cur & 1, 55)) return false;
+        if (t == 0 && h == 0 && !wait(dkv_empty, (ik & 1) ^ 1, 56)) return false;
+        sm100::tc_fence_after();
+        issue_dv(h, t == 0 && h == 0);
+        commit(do_empty(h));
+        return t + 1 >= it.T || first_s(cur + 1, h);
+      };
+      // Issue order: half 1 runs half a tile behind half 0, so that one half's softmax warps
+      // have the tensor core's results of theirs while it works for the other:
+      //   dQ_0(t-1) S2_0(t) dK_0 | dV_1(t-1) S1_1(t) | dP_0(t) dK_0 |
+      //   dQ_1(t-1) S2_1(t) dK_1 | dV_0(t) S1_0(t+1) | dP_1(t) dK_1
+      if (!(ok = first_s(tq, 0))) break;
       for (int t = 0; t < it.T && ok; ++t) {
         const uint32_t cur = tq + t;
-        const uint32_t par = cur & 1;
-        if (t > 0 && !(ok = issue_both_dq(cur - 1))) break;
-        if (!(ok = wait(s1_read, par, 52))) break;
-        sm100::tc_fence_after();
-        issue_s(cur, 1);
-        commit(s2_full);
-        if (t > 0) issue_dk(cur - 1, 0, t == 1);
-        if (!(ok = wait(do_full, par, 53))) break;
-        if (!(ok = wait(dq_empty, par ^ 1, 54))) break;
-        sm100::tc_fence_after();
-        {  // dP^T = V dO^T
-          const uint64_t ad = sm100::sdesc_sw128(vA, 16, 1024);
-          const uint64_t bd = sm100::sdesc_sw128(doA, 16, 1024);
-          if (leader) {
-#pragma unroll
-            for (int k = 0; k < DH / 16; ++k) {
-              const uint64_t o = static_cast<uint64_t>(((k >> 2) * PANEL + (k & 3) * 32) >> 4);
-              sm100::mma_ss(tmem + DP_COL, ad + o, bd + o, IDESC_S, k > 0);
-            }
-          }
-        }
-        commit(dp_full);
-        if (t > 0) {
-          issue_dk(cur - 1, 1, t == 1);
-          commit(ds_free);
-          commit(&q_empty[(cur - 1) % NQS]);
-        }
-        if (!(ok = wait(w_full, par, 55))) break;
-        if (t == 0 && !(ok = wait(dkv_empty, (ik & 1) ^ 1, 56))) break;
-        sm100::tc_fence_after();
-        if (leader) {  // dV += W^T dO: query rows 32 c ... are 16 columns from 32 c on
-#pragma unroll
-          for (int k = 0; k < BMQ / 16; ++k)
-            sm100::mma_ts(tmem + DV_COL, tmem + S_COL + (k >> 1) * 32 + (k & 1) * 8,
-                          do_mn + ((k * 2048) >> 4), C::IDESC_DV, (t > 0 || k > 0) ? 1u : 0u);
-        }
-        commit(do_empty);
-        if (t + 1 < it.T) {
-          const uint32_t nx = cur + 1;
-          if (!(ok = wait(&q_full[nx % NQS], (nx / NQS) & 1, 57))) break;
-          sm100::tc_fence_after();
-          issue_s(nx, 0);
-          commit(s1_full);
-        }
+        ok = (t == 0 || both_dq(cur - 1, 0)) && second_s(t, 0) &&
+             (t == 0 ? first_s(cur, 1) : dv_s(t - 1, 1)) && dp_dk(t, 0) &&
+             (t == 0 || both_dq(cur - 1, 1)) && second_s(t, 1) && dv_s(t, 0) && dp_dk(t, 1);
       }
       if (!ok) break;
       const uint32_t last = tq + it.T - 1;
-      if (!(ok = issue_both_dq(last))) break;
-      issue_dk(last, 0, it.T == 1);
-      issue_dk(last, 1, it.T == 1);
-      commit(ds_free);
-      commit(&q_empty[last % NQS]);
+      if (!(ok = dv_s(it.T - 1, 1))) break;
+      for (int h = 0; h < 2 && ok; ++h) {
+        if (!(ok = both_dq(last, h))) break;
+        issue_dk(last, h, 0, it.T == 1 && h == 0);
+        second_dk(last, h, it.T == 1 && h == 0);
+      }
+      if (!ok) break;
       tq += it.T;
       commit(dkv_full);
       commit(kv_empty);
@@ -531,10 +585,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
     const uint32_t s_addr = tmem + lane_base + S_COL + 32 * cq;
     const uint32_t dp_addr = tmem + lane_base + DP_COL + 32 * cq;
-    const float4* l1v = reinterpret_cast<const float4*>(smem + C::OFF_LD + cq * 128);
-    const float4* l2v = reinterpret_cast<const float4*>(smem + C::OFF_LD + 512 + cq * 128);
-    const float4* d1v = reinterpret_cast<const float4*>(smem + C::OFF_LD + 1024 + cq * 128);
-    const float4* d2v = reinterpret_cast<const float4*>(smem + C::OFF_LD + 1536 + cq * 128);
+    const int h = cq >> 1;                       // half tile of this warp's group
+    // this warp's 32 rows of the half's four statistics
+    const float4* l1v =
+        reinterpret_cast<const float4*>(smem + C::OFF_LD + h * 1024 + (cq & 1) * 128);
+    const float4 *l2v = l1v + 16, *d1v = l1v + 32, *d2v = l1v + 48;
     uint8_t* line = smem + C::OFF_DS + (cq >> 1) * PANEL + kl_ * 128;
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
     // this lane's place in an accumulator row (d = 64: only the half of the lanes whose map owns
@@ -572,12 +627,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const size_t row = static_cast<size_t>(it.b * p.Hq + it.hkv * p.G + g) * p.Lqp +
                            i * BMQ + 32 * cq;
         float* acc = p.dq_acc + row * DH + acc_lane;
-        if (!wait(dq_full, (tq + t) & 1, 65)) return false;
+        if (!wait(dq_full(h), (tq + t) & 1, 65)) return false;
         sm100::tc_fence_after();
         uint32_t v[32];
         sm100::tmem_ld32(dp_addr, v);
         sm100::tmem_ld_wait();
-        arrive(dq_empty);
+        arrive(dq_empty(h));
         if (acc_on) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) attn_bwd_impl::red_add_f32(acc + c * DH, __uint_as_float(v[c]));
@@ -614,11 +669,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           return make_float2(sm100::ex2(x.x), sm100::ex2(x.y));
         };
         // ---- P_1, kept in bf16
-        if (!(ok = wait(l_full, par, 58))) break;
-        if (!(ok = wait(s1_full, par, 59))) break;
+        if (!(ok = wait(l_full(h), par, 58))) break;
+        if (!(ok = wait(s1_full(h), par, 59))) break;
         sm100::tc_fence_after();
         load_s();
-        arrive(s1_read);
+        arrive(s1_read(h));
         mask_s();
         uint32_t p1[16];
 #pragma unroll
@@ -632,7 +687,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // ---- the previous tile's dQ
         if (t > 0 && !(ok = drain_dq(t - 1))) break;
         // ---- P_2, kept in fp32, and W = P_1 - lam P_2
-        if (!(ok = wait(s2_full, par, 60))) break;
+        if (!(ok = wait(s2_full(h), par, 60))) break;
         sm100::tc_fence_after();
         load_s();
         mask_s();
@@ -652,24 +707,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         sm100::tmem_st16(s_addr, wv);
         sm100::tmem_st_wait();
-        arrive(w_full);
+        arrive(w_full(h));
         // ---- dS_1 = P_1 (dP - D_1), dS_2 = P_2 (-lam dP + lam D_2): row-contiguous per key,
         // 16-byte chunk q of line kl_ at q ^ (kl_ & 7)
-        if (!(ok = wait(d_full, par, 61))) break;
-        if (!(ok = wait(dp_full, par, 62))) break;
-        if (!(ok = wait(ds_free, par ^ 1, 63))) break;
+        if (!(ok = wait(d_full(h), par, 61))) break;
+        if (!(ok = wait(dp_full(h), par, 62))) break;
+        if (!(ok = wait(ds_free(h), par ^ 1, 63))) break;
         sm100::tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int c16 = 0; c16 < 2; ++c16) {
           uint32_t dp[16];
-          sm100::tmem_ld16(dp_addr + 16 * h, dp);
+          sm100::tmem_ld16(dp_addr + 16 * c16, dp);
           sm100::tmem_ld_wait();
 #pragma unroll
           for (int q = 0; q < 2; ++q) {  // eight columns: one 16-byte chunk of each map
             uint32_t w1[4], w2[4];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const int cc = 4 * h + 2 * q + k;  // columns 4 cc ... of the thread's 32
+              const int cc = 4 * c16 + 2 * q + k;  // columns 4 cc ... of the thread's 32
               const float4 n1 = d1v[cc], n2 = d2v[cc];
               const float2 nd1[2] = {make_float2(n1.x, n1.y), make_float2(n1.z, n1.w)};
               const float2 ld2[2] = {make_float2(n2.x, n2.y), make_float2(n2.z, n2.w)};
@@ -685,13 +740,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 w2[2 * k + e] = sm100::pack_bf16x2(b.x, b.y);
               }
             }
-            uint8_t* at = line + (((4 * (cq & 1) + 2 * h + q) ^ (kl_ & 7)) << 4);
+            uint8_t* at = line + (((4 * (cq & 1) + 2 * c16 + q) ^ (kl_ & 7)) << 4);
             *reinterpret_cast<uint4*>(at) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
             *reinterpret_cast<uint4*>(at + 2 * PANEL) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
           }
         }
         sm100::fence_proxy_async_smem();
-        arrive(ds_full);
+        arrive(ds_full(h));
         if ((t + 1) % nq == 0) {  // the group's next head
           float x = lam_acc.x + lam_acc.y;
 #pragma unroll
@@ -827,8 +882,8 @@ attn_status_t launch_d(const Args& a, cudaStream_t s) {
     const void* g = a.Lq > 0 ? a.dO : a.K;
     const long long kvh = static_cast<long long>(a.B) * a.Hkv;
     CUtensorMap tq, tdo, tk, tv;
-    if (!attn_bwd_impl::make_tmap_rows(&tq, q, DH, a.Lq, BH, BMQ) ||
-        !attn_bwd_impl::make_tmap_rows(&tdo, g, DH, a.Lq, BH, BMQ) ||
+    if (!attn_bwd_impl::make_tmap_rows(&tq, q, DH, a.Lq, BH, HQ) ||
+        !attn_bwd_impl::make_tmap_rows(&tdo, g, DH, a.Lq, BH, HQ) ||
         !attn_bwd_impl::make_tmap_rows(&tk, a.K, DH, a.Lk, kvh, BN) ||
         !attn_bwd_impl::make_tmap_rows(&tv, a.V, DH, a.Lk, kvh, BN)) {
       attn_host::report(cudaErrorInvalidValue, "diff bwd tensor maps");
