@@ -110,6 +110,42 @@ struct Params : attn_bwd_impl::Params {
   float* lam_part;  // [n_items][G][NSMX] sums of P_2 dP
 };
 
+// sm100::mbar_wait with the slow path out of line and a longer suspension per try: the
+// waiting warps' polls otherwise take issue slots and shared-memory accesses from the others.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t a, uint32_t parity, volatile int* abort,
+                                            int* status, int site) {
+  const long long t0 = clock64();
+  for (uint32_t it = 0; it < 0x40000000u; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(a), "r"(parity), "r"(2000u)  // ns
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > ATTN_WAIT_CYCLES) break;
+  }
+  *abort = 1;
+  sm100::record_timeout(status, site);
+  return false;
+}
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                               int* status, int site) {
+  const uint32_t a = sm100::smem_u32(bar);
+  if (sm100::mbar_try_wait(a, parity)) return true;
+  return mbar_wait_slow(a, parity, abort, status, site);
+}
+
+// Four words to shared memory, free to move among loads (no memory clobber: the statistics read
+// around it lie elsewhere); later volatile statements, the proxy fence among them, stay behind.
+__device__ __forceinline__ void st_shared_v4(uint32_t at, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]));
+}
+
 // ------------------------------------------------------------------ prep
 
 // One warp per (padded) query row: D_1, D_2, the log2-LSEs and a zeroed accumulator row.
@@ -241,26 +277,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* item_full = bars + 5;   // [NI]
   uint64_t* item_empty = bars + 9;  // [NI]
   // of each half tile's pipeline h
-  auto half_bar = [&](int h, int i) -> uint64_t* { return bars + 13 + 17 * h + i; };
+  auto half_bar = [&](int h, int i) -> uint64_t* { return bars + 13 + 14 * h + i; };
   auto q_full = [&](int h, uint32_t tile) { return half_bar(h, tile % NQS); };
   auto q_empty = [&](int h, uint32_t tile) { return half_bar(h, 2 + tile % NQS); };
   auto do_full = [&](int h) { return half_bar(h, 4); };
   auto do_empty = [&](int h) { return half_bar(h, 5); };
-  auto l_full = [&](int h) { return half_bar(h, 6); };  // both -lse2 (free again once W is out)
-  auto d_full = [&](int h) { return half_bar(h, 7); };  // -D_1, lam D_2 (free once dS is out)
-  auto s1_full = [&](int h) { return half_bar(h, 8); };
-  auto s1_read = [&](int h) { return half_bar(h, 9); };
-  auto s2_full = [&](int h) { return half_bar(h, 10); };
-  auto w_full = [&](int h) { return half_bar(h, 11); };
-  auto dp_full = [&](int h) { return half_bar(h, 12); };
-  auto ds_full = [&](int h) { return half_bar(h, 13); };
-  auto ds_free = [&](int h) { return half_bar(h, 14); };  // every product has read dS
-  auto dq_full = [&](int h) { return half_bar(h, 15); };
-  auto dq_empty = [&](int h) { return half_bar(h, 16); };  // the dP columns: dQ has left
-  int* item_ring = reinterpret_cast<int*>(bars + 47);  // [NI]
+  auto s1_full = [&](int h) { return half_bar(h, 6); };  // S_1, and both -lse2 have landed
+  auto s1_read = [&](int h) { return half_bar(h, 7); };
+  auto s2_full = [&](int h) { return half_bar(h, 8); };
+  auto w_full = [&](int h) { return half_bar(h, 9); };   // frees the -lse2 as well
+  // dP, the dS buffer is free (the products of the dS before precede dP), D has landed
+  auto dp_full = [&](int h) { return half_bar(h, 10); };
+  auto ds_full = [&](int h) { return half_bar(h, 11); };  // frees the D as well
+  auto dq_full = [&](int h) { return half_bar(h, 12); };
+  auto dq_empty = [&](int h) { return half_bar(h, 13); };  // the dP columns: dQ has left
+  int* item_ring = reinterpret_cast<int*>(bars + 41);  // [NI]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_ring + NI);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(47 * 8 + NI * 4 + 8 <= 512, "barrier area");
+  static_assert(41 * 8 + NI * 4 + 8 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -281,15 +315,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       init(do_full(h), 1);
       init(do_empty(h), 1);
-      init(l_full(h), 1);
-      init(d_full(h), 1);
-      init(s1_full(h), 1);
+      init(s1_full(h), 2);  // the product's commit and the statistics' copy
       init(s1_read(h), NSMX / 2);
       init(s2_full(h), 1);
       init(w_full(h), NSMX / 2);
-      init(dp_full(h), 1);
+      init(dp_full(h), 2);
       init(ds_full(h), NSMX / 2);
-      init(ds_free(h), 1);
       init(dq_full(h), 1);
       init(dq_empty(h), NSMX / 2);
     }
@@ -312,7 +343,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t tmem = *tmem_slot;
   const int off = p.Lk - p.Lq;  // bottom-right causal alignment
   auto wait = [&](uint64_t* b, uint32_t parity, int site) -> bool {
-    return sm100::mbar_wait(b, parity, abort_flag, p.status, site);
+    return mbar_wait_long(b, parity, abort_flag, p.status, site);
   };
   auto next_item = [&](uint32_t k, int& w) -> bool {
     if (!wait(&item_full[k % NI], (k / NI) & 1, 41)) return false;
@@ -387,8 +418,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           const uint32_t par = (tq & 1) ^ 1;
           const float* st = p.stats + (static_cast<size_t>(qh) * p.n_qt + i) * 512 + h * 256;
           if (!(ok = wait(w_full(h), par, 45))) break;
-          sm100::mbar_arrive_expect_tx(l_full(h), 512);
-          attn_bwd_impl::bulk_g2s(ld, st, 512, l_full(h));
+          sm100::mbar_arrive_expect_tx(s1_full(h), 512);
+          attn_bwd_impl::bulk_g2s(ld, st, 512, s1_full(h));
           ++n_l;
           if (!(ok = wait(do_empty(h), par, 46))) break;
           sm100::mbar_arrive_expect_tx(do_full(h), C::TILE / 2);
@@ -397,17 +428,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                i * BMQ + h * HQ, qh);
           ++n_do;
           if (!(ok = wait(ds_full(h), par, 47))) break;
-          sm100::mbar_arrive_expect_tx(d_full(h), 512);
-          attn_bwd_impl::bulk_g2s(ld + 512, st + 128, 512, d_full(h));
+          sm100::mbar_arrive_expect_tx(dp_full(h), 512);
+          attn_bwd_impl::bulk_g2s(ld + 512, st + 128, 512, dp_full(h));
           ++n_d;
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     if (sm100::lane_id() == 0) {
-      if (n_l > 0) sm100::mbar_wait_drain(l_full(h), (n_l - 1) & 1);
+      if (n_l > 0) sm100::mbar_wait_drain(s1_full(h), (n_l - 1) & 1);
       if (n_do > 0) sm100::mbar_wait_drain(do_full(h), (n_do - 1) & 1);
-      if (n_d > 0) sm100::mbar_wait_drain(d_full(h), (n_d - 1) & 1);
+      if (n_d > 0) sm100::mbar_wait_drain(dp_full(h), (n_d - 1) & 1);
     }
   } else if (warp == W_MMA) {
     // ------------------------------------------------------------ MMA issuer
@@ -518,29 +549,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         commit(dq_full(h));
         return true;
       };
-      // S_2 of the half's tile t, with the first dK of its tile t - 1 behind it
+      // S_2 of the half's tile t, with both dK of its tile t - 1 behind it
+      auto both_dk = [&](uint32_t tile, int h, bool first) {
+        issue_dk(tile, h, 0, first);
+        issue_dk(tile, h, 1, first);
+        commit(q_empty(h, tile));
+      };
       auto second_s = [&](int t, int h) -> bool {
         const uint32_t cur = tq + t;
         if (!wait(s1_read(h), cur & 1, 52)) return false;
         sm100::tc_fence_after();
         issue_s(cur, h, 1);
         commit(s2_full(h));
-        if (t > 0) issue_dk(cur - 1, h, 0, t == 1 && h == 0);
+        if (t > 0) both_dk(cur - 1, h, t == 1 && h == 0);
         return true;
       };
-      auto second_dk = [&](uint32_t tile, int h, bool first) {
-        issue_dk(tile, h, 1, first);
-        commit(ds_free(h));
-        commit(q_empty(h, tile));
-      };
-      auto dp_dk = [&](int t, int h) -> bool {
+      auto first_dp = [&](int t, int h) -> bool {
         const uint32_t cur = tq + t;
         if (!wait(do_full(h), cur & 1, 53)) return false;
         if (!wait(dq_empty(h), (cur & 1) ^ 1, 54)) return false;
         sm100::tc_fence_after();
         issue_dp(h);
         commit(dp_full(h));
-        if (t > 0) second_dk(cur - 1, h, t == 1 && h == 0);
         return true;
       };
       auto dv_s = [&](int t, int h) -> bool {
@@ -554,22 +584,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       };
       // Issue order: half 1 runs half a tile behind half 0, so that one half's softmax warps
       // have the tensor core's results of theirs while it works for the other:
-      //   dQ_0(t-1) S2_0(t) dK_0 | dV_1(t-1) S1_1(t) | dP_0(t) dK_0 |
-      //   dQ_1(t-1) S2_1(t) dK_1 | dV_0(t) S1_0(t+1) | dP_1(t) dK_1
+      //   dQ_0(t-1) S2_0(t) dK_0 | dV_1(t-1) S1_1(t) | dP_0(t) |
+      //   dQ_1(t-1) S2_1(t) dK_1 | dV_0(t) S1_0(t+1) | dP_1(t)
       if (!(ok = first_s(tq, 0))) break;
       for (int t = 0; t < it.T && ok; ++t) {
         const uint32_t cur = tq + t;
         ok = (t == 0 || both_dq(cur - 1, 0)) && second_s(t, 0) &&
-             (t == 0 ? first_s(cur, 1) : dv_s(t - 1, 1)) && dp_dk(t, 0) &&
-             (t == 0 || both_dq(cur - 1, 1)) && second_s(t, 1) && dv_s(t, 0) && dp_dk(t, 1);
+             (t == 0 ? first_s(cur, 1) : dv_s(t - 1, 1)) && first_dp(t, 0) &&
+             (t == 0 || both_dq(cur - 1, 1)) && second_s(t, 1) && dv_s(t, 0) && first_dp(t, 1);
       }
       if (!ok) break;
       const uint32_t last = tq + it.T - 1;
       if (!(ok = dv_s(it.T - 1, 1))) break;
       for (int h = 0; h < 2 && ok; ++h) {
         if (!(ok = both_dq(last, h))) break;
-        issue_dk(last, h, 0, it.T == 1 && h == 0);
-        second_dk(last, h, it.T == 1 && h == 0);
+        both_dk(last, h, it.T == 1 && h == 0);
       }
       if (!ok) break;
       tq += it.T;
@@ -590,7 +619,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const float4* l1v =
         reinterpret_cast<const float4*>(smem + C::OFF_LD + h * 1024 + (cq & 1) * 128);
     const float4 *l2v = l1v + 16, *d1v = l1v + 32, *d2v = l1v + 48;
-    uint8_t* line = smem + C::OFF_DS + (cq >> 1) * PANEL + kl_ * 128;
+    const uint32_t line = sbase + C::OFF_DS + (cq >> 1) * PANEL + kl_ * 128;
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
     // this lane's place in an accumulator row (d = 64: only the half of the lanes whose map owns
     // this quarter's columns)
@@ -620,14 +649,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (it.T == 0 && sm100::lane_id() == 0)
         for (int g = 0; g < p.G; ++g) lam_part[g * NSMX + warp] = 0.f;
       float2 lam_acc = make_float2(0.f, 0.f);
+      // query head g of the group and query tile i of the t-th tile (as tile_of, without its
+      // divisions), this warp's place in the accumulator there and in the tile before
+      int g = 0, i = it.i_lo;
+      const float* lam = p.lam + (p.n_lam == 1 ? 0 : it.hkv * p.G);
+      float nl_h = -__ldg(lam);
+      const int i_end = it.i_lo + nq;
+      float* acc = p.dq_acc + acc_lane +
+                   (static_cast<size_t>(it.b * p.Hq + it.hkv * p.G) * p.Lqp + i * BMQ + 32 * cq) * DH;
+      float* acc_prev = acc;
+      const size_t head_skip = static_cast<size_t>(p.Lqp - nq * BMQ) * DH;
       // adds this warp's 32 rows of a tile's dQ^T (lanes = head dimension) into the accumulator
-      auto drain_dq = [&](int t) -> bool {
-        int g, i;
-        tile_of(it, t, nq, g, i);
-        const size_t row = static_cast<size_t>(it.b * p.Hq + it.hkv * p.G + g) * p.Lqp +
-                           i * BMQ + 32 * cq;
-        float* acc = p.dq_acc + row * DH + acc_lane;
-        if (!wait(dq_full(h), (tq + t) & 1, 65)) return false;
+      auto drain_dq = [&](uint32_t tile) -> bool {
+        if (!wait(dq_full(h), tile & 1, 65)) return false;
         sm100::tc_fence_after();
         uint32_t v[32];
         sm100::tmem_ld32(dp_addr, v);
@@ -635,16 +669,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         arrive(dq_empty(h));
         if (acc_on) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) attn_bwd_impl::red_add_f32(acc + c * DH, __uint_as_float(v[c]));
+          for (int c = 0; c < 32; ++c)
+            attn_bwd_impl::red_add_f32(acc_prev + c * DH, __uint_as_float(v[c]));
         }
         return true;
       };
       for (int t = 0; t < it.T && ok; ++t) {
         const uint32_t par = (tq + t) & 1;
-        int g, i;
-        tile_of(it, t, nq, g, i);
-        const float lam = __ldg(p.lam + (p.n_lam == 1 ? 0 : it.hkv * p.G + g));
-        const float2 nlam = make_float2(-lam, -lam);
+        const float2 nlam = make_float2(nl_h, nl_h);
         // key visible to query row r0 + c iff key < kv_len and c >= cmin
         const bool key_ok = key < it.kv_len;
         const int cmin = p.causal ? key - (i * BMQ + 32 * cq) - off : -1;
@@ -669,7 +701,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           return make_float2(sm100::ex2(x.x), sm100::ex2(x.y));
         };
         // ---- P_1, kept in bf16
-        if (!(ok = wait(l_full(h), par, 58))) break;
         if (!(ok = wait(s1_full(h), par, 59))) break;
         sm100::tc_fence_after();
         load_s();
@@ -685,7 +716,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           p1[2 * c4 + 1] = sm100::pack_bf16x2(e1.x, e1.y);
         }
         // ---- the previous tile's dQ
-        if (t > 0 && !(ok = drain_dq(t - 1))) break;
+        if (t > 0 && !(ok = drain_dq(tq + t - 1))) break;
         // ---- P_2, kept in fp32, and W = P_1 - lam P_2
         if (!(ok = wait(s2_full(h), par, 60))) break;
         sm100::tc_fence_after();
@@ -710,9 +741,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         arrive(w_full(h));
         // ---- dS_1 = P_1 (dP - D_1), dS_2 = P_2 (-lam dP + lam D_2): row-contiguous per key,
         // 16-byte chunk q of line kl_ at q ^ (kl_ & 7)
-        if (!(ok = wait(d_full(h), par, 61))) break;
         if (!(ok = wait(dp_full(h), par, 62))) break;
-        if (!(ok = wait(ds_free(h), par ^ 1, 63))) break;
         sm100::tc_fence_after();
 #pragma unroll
         for (int c16 = 0; c16 < 2; ++c16) {
@@ -740,23 +769,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 w2[2 * k + e] = sm100::pack_bf16x2(b.x, b.y);
               }
             }
-            uint8_t* at = line + (((4 * (cq & 1) + 2 * c16 + q) ^ (kl_ & 7)) << 4);
-            *reinterpret_cast<uint4*>(at) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-            *reinterpret_cast<uint4*>(at + 2 * PANEL) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+            const uint32_t at = line + (((4 * (cq & 1) + 2 * c16 + q) ^ (kl_ & 7)) << 4);
+            st_shared_v4(at, w1);
+            st_shared_v4(at + 2 * PANEL, w2);
           }
         }
         sm100::fence_proxy_async_smem();
         arrive(ds_full(h));
-        if ((t + 1) % nq == 0) {  // the group's next head
+        acc_prev = acc;
+        acc += BMQ * DH;
+        if (++i == i_end) {  // the group's next head
           float x = lam_acc.x + lam_acc.y;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
           if (sm100::lane_id() == 0) lam_part[g * NSMX + warp] = x;
           lam_acc = make_float2(0.f, 0.f);
+          acc += head_skip;
+          i = it.i_lo;
+          if (++g < p.G && p.n_lam != 1) nl_h = -__ldg(lam + g);
         }
       }
       if (!ok) break;
-      if (it.T > 0 && !(ok = drain_dq(it.T - 1))) break;
+      if (it.T > 0 && !(ok = drain_dq(tq + it.T - 1))) break;
       tq += it.T;
       // ---------------- epilogue: dV, dK (x scale) of this key row, a quarter of the columns
       if (!(ok = wait(dkv_full, ik & 1, 64))) break;
