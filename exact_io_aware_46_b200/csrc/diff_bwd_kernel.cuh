@@ -10,13 +10,14 @@
 // One pass forms both maps from one read of Q, dO, K and V: five GEMMs' worth of
 // MMA work per tile, as for one map of the full width, with one dP and one dV
 // product instead of two.  Launches, work items (128 keys of one batch and
-// key/value head) and their order are those of bwd_kernel.cuh; per 128-row query
-// tile, keys on the 128 TMEM lanes (the tile's columns are query rows):
+// key/value head) and their order are those of bwd_kernel.cuh; a 128-row query tile
+// is worked as two halves of 64 rows in turn, with keys on the 128 TMEM lanes (a
+// half's columns are query rows):
 //   S_1^T, S_2^T = K_m Q_m^T   (SS, half the K steps each, one after the other in
-//                               the same 128 columns: the softmax reads S_1 out
-//                               before S_2 is issued)
-//   dP^T = V dO^T              (SS, 128 columns)
-//   dV  += W^T dO              (TS, W = P_1 - lam P_2 in bf16 over the S columns)
+//                               the half's 64 columns: S_1 is read out before S_2
+//                               is issued)
+//   dP^T = V dO^T              (SS, 64 columns)
+//   dV  += W^T dO              (TS, W = P_1 - lam P_2 in bf16 over the dP columns)
 //   dK_m += dS_m^T Q_m         (SS, N = 64, dS_m staged in shared memory)
 //   dQ_m^T = K_m^T dS_m^T      (SS, M = 64, lanes = head dimension, over the dP columns:
 //                               map 1 in lanes 0-15 of each 32, map 2 in lanes 16-31)
@@ -25,23 +26,30 @@
 // 64-column panel -- with N this small an SS product is bound by reading A, and M has
 // no smaller value -- and the half that belongs to the other map is not read.
 //
-// Warps 0-15 form P, W and dS (a key row per thread, four warps per row with 32
-// query rows each) and between P_1 and P_2 add the previous tile's dQ^T into the
-// fp32 accumulator, 32 of its columns a warp, with 4-byte reductions that cover 128
-// contiguous bytes (the accumulator's columns are ordered as the lanes are); warp
-// 16 feeds TMA, warp 17 issues the MMAs.  The additions happen at L2, whose rate
-// bounds the kernel at d = 128: 64 KB per tile and SM take 2.1 us whichever way they
-// are sent (measured: reductions of 4 bytes a lane 4628 GB/s, bulk reduce-adds 4593,
-// tensor reduce-adds 4312, 16 bytes a lane with a row per lane 2484), so the way that
-// needs no shared memory was taken: staging dQ in the dS buffers, the only room left,
-// tied each tile's dS to the reduce-adds of the last (2715 us on causal B2 H16 L8192).
+// Warps 0-7 and 8-15 work half 0 and half 1, half a tile apart: one group's scalar
+// work (a key row per thread, two warps per row) runs while the tensor core works
+// for the other.  Per half and tile a group forms P_1, adds the tile before's dQ^T
+// into the fp32 accumulator, and then forms P_2, W and both dS sixteen columns at a
+// time, dP at hand, so that 96 registers hold it all.  dQ^T goes out by 4-byte reductions
+// that cover 128 contiguous bytes (the accumulator's columns are ordered as the lanes
+// are).  Those additions happen at L2, at a rate that no way of sending them changed
+// (64 KB per tile and SM in 2.1 us: reductions of 4 bytes a lane 4628 GB/s, bulk
+// reduce-adds 4593, tensor reduce-adds 4312; 16 bytes a lane with a row per lane 2484),
+// so the way that needs no shared memory was taken.  Warp 16 feeds K, V and Q by TMA,
+// warps 18 and 19 a half's statistics and dO each, warp 17 issues the MMAs.
+//
+// Measured on B200 (causal B2 H16 L8192 d128): dQ staged in the dS buffers and one tile
+// at a time 2715 us; dQ by reductions 2392; halves in turn 2031; fewer waits and no
+// divisions 1869; P_2 and dS in one go 1701.
 //
 // dlam needs more of P_2 than bf16 gives: its terms P_2 dP have both signs, and
 // the roundings of P_2 (2^-9 relative on average) do not shrink with the sum.
-// P_2 is therefore kept in fp32 until dP is there.  Sums per (item, head,
+// The sums take P_2 in fp32, as it comes from the exponential.  Sums per (item, head,
 // warp) go to the workspace and are added in a fixed order, so dlam is the same
 // from run to run.
 #pragma once
+
+#include <climits>
 
 #include "bwd_kernel.cuh"
 
@@ -100,8 +108,9 @@ constexpr uint32_t DP_COL = 128;  // dP^T, then dQ_1^T and dQ_2^T in alternate 1
 constexpr uint32_t DV_COL = 256;
 constexpr uint32_t DK_COL = 384;  // dK_1, dK_2 (64 each)
 
-// Column pairs cp of a 16-pair block with (cp & 7) >= POLY_FROM take the FMA-pipe exp2.
-constexpr int POLY_FROM = 8;
+// All exponentials are on the special-function unit: with polynomials for an eighth or a quarter
+// of them the kernel ran 2 to 4 % slower (causal B2 H16 L8192 d128), as issue slots, not that
+// unit, are short.
 
 struct Params : attn_bwd_impl::Params {
   const float* stats;  // [B*Hq][n_qt][2 halves][4][64]: -lse2_1, -lse2_2, -D_1, lam D_2
@@ -132,9 +141,8 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t a, uint32_t parity, volatil
   sm100::record_timeout(status, site);
   return false;
 }
-__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                               int* status, int site) {
-  const uint32_t a = sm100::smem_u32(bar);
+__device__ __forceinline__ bool mbar_wait_at(uint32_t a, uint32_t parity, volatile int* abort,
+                                             int* status, int site) {
   if (sm100::mbar_try_wait(a, parity)) return true;
   return mbar_wait_slow(a, parity, abort, status, site);
 }
@@ -277,24 +285,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* item_full = bars + 5;   // [NI]
   uint64_t* item_empty = bars + 9;  // [NI]
   // of each half tile's pipeline h
-  auto half_bar = [&](int h, int i) -> uint64_t* { return bars + 13 + 14 * h + i; };
+  auto half_bar = [&](int h, int i) -> uint64_t* { return bars + 13 + 13 * h + i; };
   auto q_full = [&](int h, uint32_t tile) { return half_bar(h, tile % NQS); };
   auto q_empty = [&](int h, uint32_t tile) { return half_bar(h, 2 + tile % NQS); };
   auto do_full = [&](int h) { return half_bar(h, 4); };
   auto do_empty = [&](int h) { return half_bar(h, 5); };
-  auto s1_full = [&](int h) { return half_bar(h, 6); };  // S_1, and both -lse2 have landed
+  auto s1_full = [&](int h) { return half_bar(h, 6); };  // S_1, and -lse2_1 has landed
   auto s1_read = [&](int h) { return half_bar(h, 7); };
-  auto s2_full = [&](int h) { return half_bar(h, 8); };
-  auto w_full = [&](int h) { return half_bar(h, 9); };   // frees the -lse2 as well
-  // dP, the dS buffer is free (the products of the dS before precede dP), D has landed
-  auto dp_full = [&](int h) { return half_bar(h, 10); };
-  auto ds_full = [&](int h) { return half_bar(h, 11); };  // frees the D as well
-  auto dq_full = [&](int h) { return half_bar(h, 12); };
-  auto dq_empty = [&](int h) { return half_bar(h, 13); };  // the dP columns: dQ has left
-  int* item_ring = reinterpret_cast<int*>(bars + 41);  // [NI]
+  auto s2_read = [&](int h) { return half_bar(h, 8); };  // frees the -lse2_1 as well
+  // dP and S_2, the dS buffer is free (the products of the dS before precede dP), and the
+  // other three statistics have landed
+  auto dp_full = [&](int h) { return half_bar(h, 9); };
+  auto ds_full = [&](int h) { return half_bar(h, 10); };  // dS and W; frees those three
+  auto dq_full = [&](int h) { return half_bar(h, 11); };
+  auto dq_empty = [&](int h) { return half_bar(h, 12); };  // the dP columns: dQ has left
+  int* item_ring = reinterpret_cast<int*>(bars + 39);  // [NI]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_ring + NI);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(41 * 8 + NI * 4 + 8 <= 512, "barrier area");
+  static_assert(39 * 8 + NI * 4 + 8 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -317,8 +325,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       init(do_empty(h), 1);
       init(s1_full(h), 2);  // the product's commit and the statistics' copy
       init(s1_read(h), NSMX / 2);
-      init(s2_full(h), 1);
-      init(w_full(h), NSMX / 2);
+      init(s2_read(h), NSMX / 2);
       init(dp_full(h), 2);
       init(ds_full(h), NSMX / 2);
       init(dq_full(h), 1);
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t tmem = *tmem_slot;
   const int off = p.Lk - p.Lq;  // bottom-right causal alignment
   auto wait = [&](uint64_t* b, uint32_t parity, int site) -> bool {
-    return mbar_wait_long(b, parity, abort_flag, p.status, site);
+    return mbar_wait_at(sm100::smem_u32(b), parity, abort_flag, p.status, site);
   };
   auto next_item = [&](uint32_t k, int& w) -> bool {
     if (!wait(&item_full[k % NI], (k / NI) & 1, 41)) return false;
@@ -417,20 +424,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           const int qh = it.b * p.Hq + it.hkv * p.G + g;
           const uint32_t par = (tq & 1) ^ 1;
           const float* st = p.stats + (static_cast<size_t>(qh) * p.n_qt + i) * 512 + h * 256;
-          if (!(ok = wait(w_full(h), par, 45))) break;
-          sm100::mbar_arrive_expect_tx(s1_full(h), 512);
-          attn_bwd_impl::bulk_g2s(ld, st, 512, s1_full(h));
+          if (!(ok = wait(s2_read(h), par, 45))) break;
+          sm100::mbar_arrive_expect_tx(s1_full(h), 256);
+          attn_bwd_impl::bulk_g2s(ld, st, 256, s1_full(h));
           ++n_l;
+          if (!(ok = wait(ds_full(h), par, 47))) break;
+          sm100::mbar_arrive_expect_tx(dp_full(h), 768);
+          attn_bwd_impl::bulk_g2s(ld + 256, st + 64, 768, dp_full(h));
+          ++n_d;
           if (!(ok = wait(do_empty(h), par, 46))) break;
           sm100::mbar_arrive_expect_tx(do_full(h), C::TILE / 2);
           for (int c = 0; c < C::PANELS; ++c)
             sm100::tma_load_3d(&tmdO, do_full(h), smem + C::OFF_DO + c * PANEL + h * HROWS, c * 64,
                                i * BMQ + h * HQ, qh);
           ++n_do;
-          if (!(ok = wait(ds_full(h), par, 47))) break;
-          sm100::mbar_arrive_expect_tx(dp_full(h), 512);
-          attn_bwd_impl::bulk_g2s(ld + 512, st + 128, 512, dp_full(h));
-          ++n_d;
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -479,7 +486,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (leader) {
 #pragma unroll
         for (int k = 0; k < HQ / 16; ++k)
-          sm100::mma_ts(tmem + DV_COL, tmem + S_COL + HQ * h + (k >> 1) * 32 + (k & 1) * 8,
+          sm100::mma_ts(tmem + DV_COL, tmem + DP_COL + HQ * h + (k >> 1) * 32 + (k & 1) * 8,
                         bd + ((k * 2048) >> 4), C::IDESC_DV, (!first || k > 0) ? 1u : 0u);
       }
     };
@@ -532,8 +539,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         continue;
       }
       if (it.kv_len < p.Lk && it.kv_len < (it.n + 1) * BN) clear_tail(it.kv_len - it.n * BN);
-      // the first product of a half's tile, as soon as its Q is there (its S columns are free:
-      // the half's dV before has been issued)
+      // S_1 of a half's tile (its S columns are free: S_2 of the tile before has been read)
       auto first_s = [&](uint32_t tile, int h) -> bool {
         if (!wait(q_full(h, tile), (tile / NQS) & 1, 50)) return false;
         sm100::tc_fence_after();
@@ -541,27 +547,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         commit(s1_full(h));
         return true;
       };
-      auto both_dq = [&](uint32_t tile, int h) -> bool {
-        if (!wait(ds_full(h), tile & 1, 51)) return false;
+      // dV of W and then both dQ of dS, over the columns that W was in
+      auto dv_dq = [&](int t, int h) -> bool {
+        if (!wait(ds_full(h), (tq + t) & 1, 51)) return false;
+        const bool first = t == 0 && h == 0;
+        if (first && !wait(dkv_empty, (ik & 1) ^ 1, 56)) return false;
         sm100::tc_fence_after();
+        issue_dv(h, first);
+        commit(do_empty(h));
         issue_dq(h, 0);
         issue_dq(h, 1);
         commit(dq_full(h));
         return true;
       };
-      // S_2 of the half's tile t, with both dK of its tile t - 1 behind it
-      auto both_dk = [&](uint32_t tile, int h, bool first) {
-        issue_dk(tile, h, 0, first);
-        issue_dk(tile, h, 1, first);
-        commit(q_empty(h, tile));
+      auto both_dk = [&](int t, int h) {
+        const bool first = t == 0 && h == 0;
+        issue_dk(tq + t, h, 0, first);
+        issue_dk(tq + t, h, 1, first);
+        commit(q_empty(h, tq + t));
       };
       auto second_s = [&](int t, int h) -> bool {
-        const uint32_t cur = tq + t;
-        if (!wait(s1_read(h), cur & 1, 52)) return false;
+        if (!wait(s1_read(h), (tq + t) & 1, 52)) return false;
         sm100::tc_fence_after();
-        issue_s(cur, h, 1);
-        commit(s2_full(h));
-        if (t > 0) both_dk(cur - 1, h, t == 1 && h == 0);
+        issue_s(tq + t, h, 1);
+        if (t > 0) both_dk(t - 1, h);
         return true;
       };
       auto first_dp = [&](int t, int h) -> bool {
@@ -573,32 +582,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         commit(dp_full(h));
         return true;
       };
-      auto dv_s = [&](int t, int h) -> bool {
-        const uint32_t cur = tq + t;
-        if (!wait(w_full(h), cur & 1, 55)) return false;
-        if (t == 0 && h == 0 && !wait(dkv_empty, (ik & 1) ^ 1, 56)) return false;
-        sm100::tc_fence_after();
-        issue_dv(h, t == 0 && h == 0);
-        commit(do_empty(h));
-        return t + 1 >= it.T || first_s(cur + 1, h);
+      auto next_s = [&](int t, int h) -> bool {
+        if (t + 1 >= it.T) return true;
+        return wait(s2_read(h), (tq + t) & 1, 55) && first_s(tq + t + 1, h);
       };
       // Issue order: half 1 runs half a tile behind half 0, so that one half's softmax warps
       // have the tensor core's results of theirs while it works for the other:
-      //   dQ_0(t-1) S2_0(t) dK_0 | dV_1(t-1) S1_1(t) | dP_0(t) |
-      //   dQ_1(t-1) S2_1(t) dK_1 | dV_0(t) S1_0(t+1) | dP_1(t)
+      //   dV_0 dQ_0(t-1) S2_0(t) dK_0(t-1) | S1_1(t) | dP_0(t) |
+      //   dV_1 dQ_1(t-1) S2_1(t) dK_1(t-1) | S1_0(t+1) | dP_1(t)
       if (!(ok = first_s(tq, 0))) break;
-      for (int t = 0; t < it.T && ok; ++t) {
-        const uint32_t cur = tq + t;
-        ok = (t == 0 || both_dq(cur - 1, 0)) && second_s(t, 0) &&
-             (t == 0 ? first_s(cur, 1) : dv_s(t - 1, 1)) && first_dp(t, 0) &&
-             (t == 0 || both_dq(cur - 1, 1)) && second_s(t, 1) && dv_s(t, 0) && first_dp(t, 1);
-      }
-      if (!ok) break;
-      const uint32_t last = tq + it.T - 1;
-      if (!(ok = dv_s(it.T - 1, 1))) break;
+      for (int t = 0; t < it.T && ok; ++t)
+        ok = (t == 0 || dv_dq(t - 1, 0)) && second_s(t, 0) &&
+             (t == 0 ? first_s(tq, 1) : next_s(t - 1, 1)) && first_dp(t, 0) &&
+             (t == 0 || dv_dq(t - 1, 1)) && second_s(t, 1) && next_s(t, 0) && first_dp(t, 1);
       for (int h = 0; h < 2 && ok; ++h) {
-        if (!(ok = both_dq(last, h))) break;
-        both_dk(last, h, it.T == 1 && h == 0);
+        if (!(ok = dv_dq(it.T - 1, h))) break;
+        both_dk(it.T - 1, h);
       }
       if (!ok) break;
       tq += it.T;
@@ -609,29 +608,35 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     sm100::mbar_wait_drain(drain, 0);
   } else {
     // ------------------------------------------------------------ P, W and dS; dQ
-    const int qd = warp & 3, cq = warp >> 2;
-    const int kl_ = qd * 32 + sm100::lane_id();  // key row within the tile = TMEM lane
-    const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
-    const uint32_t s_addr = tmem + lane_base + S_COL + 32 * cq;
-    const uint32_t dp_addr = tmem + lane_base + DP_COL + 32 * cq;
-    const int h = cq >> 1;                       // half tile of this warp's group
+    // Little state is kept across tiles (barriers as 32-bit addresses, one accumulator
+    // pointer, the mask as one bound): 96 registers hold 48 of probabilities.
+    const int qd = warp & 3, cq = warp >> 2, lane = sm100::lane_id();
+    const int h = cq >> 1;  // half tile of this warp's group
+    const int kl_ = qd * 32 + lane;  // key row within the tile = TMEM lane
+    const uint32_t s_addr = tmem + (static_cast<uint32_t>(qd * 32) << 16) + S_COL + 32 * cq;
+    const uint32_t dp_addr = s_addr + (DP_COL - S_COL);
+    const uint32_t hb = sm100::smem_u32(half_bar(h, 0));
+    constexpr uint32_t S1_FULL = 6 * 8, S1_READ = 7 * 8, S2_READ = 8 * 8, DP_FULL = 9 * 8,
+                       DS_FULL = 10 * 8, DQ_FULL = 11 * 8, DQ_EMPTY = 12 * 8;
     // this warp's 32 rows of the half's four statistics
     const float4* l1v =
         reinterpret_cast<const float4*>(smem + C::OFF_LD + h * 1024 + (cq & 1) * 128);
     const float4 *l2v = l1v + 16, *d1v = l1v + 32, *d2v = l1v + 48;
-    const uint32_t line = sbase + C::OFF_DS + (cq >> 1) * PANEL + kl_ * 128;
-    const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+    // its 64 bytes of this key row's dS line
+    const uint32_t line = sbase + C::OFF_DS + h * PANEL + kl_ * 128;
     // this lane's place in an accumulator row (d = 64: only the half of the lanes whose map owns
     // this quarter's columns)
-    const int lane = sm100::lane_id();
-    const int acc_lane = DH == 128 ? 32 * qd + lane : 16 * qd + (lane & 15);
     const bool acc_on = DH == 128 || (lane >> 4) == (qd >> 1);
-    uint32_t tq = 0;
+    uint32_t cur = 0;  // query tiles done
     bool ok = true;
-    auto arrive = [&](uint64_t* bar) {
+    auto wait_at = [&](uint32_t bar, uint32_t tile, int site) -> bool {
+      return mbar_wait_at(hb + bar, tile & 1, abort_flag, p.status, site);
+    };
+    auto arrive_at = [&](uint32_t bar) {
       sm100::tc_fence_before();
       __syncwarp();
-      if (sm100::lane_id() == 0) sm100::mbar_arrive(bar);
+      if (sm100::lane_id() == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(hb + bar) : "memory");
     };
     auto f2 = [](uint32_t a, uint32_t b) {
       return make_float2(__uint_as_float(a), __uint_as_float(b));
@@ -642,161 +647,135 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       bool bad = false;
       const Item it = get_item(p, w, &bad);
       if (bad && threadIdx.x == 0) atomicOr(p.status, 1);
+      const int kvh = it.b * p.Hkv + it.hkv;
       const int key = it.n * BN + kl_;
-      const int nq = it.T > 0 ? it.T / p.G : 0;
-      float* lam_part =
-          p.lam_part + ((static_cast<size_t>(it.b) * p.Hkv + it.hkv) * p.n_kv + it.n) * p.G * NSMX;
-      if (it.T == 0 && sm100::lane_id() == 0)
-        for (int g = 0; g < p.G; ++g) lam_part[g * NSMX + warp] = 0.f;
-      float2 lam_acc = make_float2(0.f, 0.f);
-      // query head g of the group and query tile i of the t-th tile (as tile_of, without its
-      // divisions), this warp's place in the accumulator there and in the tile before
-      int g = 0, i = it.i_lo;
-      const float* lam = p.lam + (p.n_lam == 1 ? 0 : it.hkv * p.G);
-      float nl_h = -__ldg(lam);
-      const int i_end = it.i_lo + nq;
-      float* acc = p.dq_acc + acc_lane +
-                   (static_cast<size_t>(it.b * p.Hq + it.hkv * p.G) * p.Lqp + i * BMQ + 32 * cq) * DH;
-      float* acc_prev = acc;
-      const size_t head_skip = static_cast<size_t>(p.Lqp - nq * BMQ) * DH;
+      // query row r0 + c (r0 the warp's first row of tile i) sees the key iff c >= cmin0 - 128 i
+      // (causal), for every c or for none
+      const int cmin0 = key >= it.kv_len ? INT_MAX : p.causal ? key - off - 32 * cq : INT_MIN / 2;
+      const int cstep = p.causal ? BMQ : 0;
+      const int i_end = it.i_lo + (it.T > 0 ? it.T / p.G : 0);
+      // where the next dQ goes
+      float* acc = p.dq_acc + (DH == 128 ? 32 * qd + lane : 16 * qd + (lane & 15)) +
+                   (static_cast<size_t>(it.b * p.Hq + it.hkv * p.G) * p.Lqp + it.i_lo * BMQ + 32 * cq) * DH;
       // adds this warp's 32 rows of a tile's dQ^T (lanes = head dimension) into the accumulator
       auto drain_dq = [&](uint32_t tile) -> bool {
-        if (!wait(dq_full(h), tile & 1, 65)) return false;
+        if (!wait_at(DQ_FULL, tile, 65)) return false;
         sm100::tc_fence_after();
         uint32_t v[32];
         sm100::tmem_ld32(dp_addr, v);
         sm100::tmem_ld_wait();
-        arrive(dq_empty(h));
+        arrive_at(DQ_EMPTY);
         if (acc_on) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            attn_bwd_impl::red_add_f32(acc_prev + c * DH, __uint_as_float(v[c]));
+          for (int c = 0; c < 32; ++c) attn_bwd_impl::red_add_f32(acc + c * DH, __uint_as_float(v[c]));
         }
+        acc += BMQ * DH;
         return true;
       };
-      for (int t = 0; t < it.T && ok; ++t) {
-        const uint32_t par = (tq + t) & 1;
-        const float2 nlam = make_float2(nl_h, nl_h);
-        // key visible to query row r0 + c iff key < kv_len and c >= cmin
-        const bool key_ok = key < it.kv_len;
-        const int cmin = p.causal ? key - (i * BMQ + 32 * cq) - off : -1;
-        const bool all_vis = __all_sync(0xffffffffu, key_ok && cmin <= 0);
-        uint32_t s[32];
-        // scores of one map out of TMEM, masked
-        auto load_s = [&] {
-          sm100::tmem_ld32(s_addr, s);
-          sm100::tmem_ld_wait();
-        };
-        auto mask_s = [&] {
-          if (!all_vis) {
+      for (int g = 0; g < p.G && ok; ++g) {
+        float2 lam_acc = make_float2(0.f, 0.f);
+        const float nl = -__ldg(p.lam + (p.n_lam == 1 ? 0 : it.hkv * p.G + g));
+        for (int i = it.i_lo; i < i_end; ++i, ++cur) {
+          const int cmin = cmin0 - i * cstep;
+          const bool all_vis = __all_sync(0xffffffffu, cmin <= 0);
+          const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nlam = make_float2(nl, nl);
+          // ---- P_1, kept in bf16
+          if (!(ok = wait_at(S1_FULL, cur, 59))) break;
+          sm100::tc_fence_after();
+          uint32_t p1[16];
+          {
+            uint32_t s[32];
+            sm100::tmem_ld32(s_addr, s);
+            sm100::tmem_ld_wait();
+            arrive_at(S1_READ);
+            if (!all_vis) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!key_ok || c < cmin) s[c] = __float_as_uint(-INFINITY);
-          }
-        };
-        // exponentials of column pair cp
-        auto prob = [&](int cp, float2 nl) -> float2 {
-          const float2 x = __ffma2_rn(f2(s[2 * cp], s[2 * cp + 1]), sl2, nl);
-          if ((cp & 7) >= POLY_FROM) return sm100::ex2_poly2(x);
-          return make_float2(sm100::ex2(x.x), sm100::ex2(x.y));
-        };
-        // ---- P_1, kept in bf16
-        if (!(ok = wait(s1_full(h), par, 59))) break;
-        sm100::tc_fence_after();
-        load_s();
-        arrive(s1_read(h));
-        mask_s();
-        uint32_t p1[16];
+              for (int c = 0; c < 32; ++c)
+                if (c < cmin) s[c] = __float_as_uint(-INFINITY);
+            }
 #pragma unroll
-        for (int c4 = 0; c4 < 8; ++c4) {
-          const float4 nl = l1v[c4];
-          const float2 e0 = prob(2 * c4, make_float2(nl.x, nl.y));
-          const float2 e1 = prob(2 * c4 + 1, make_float2(nl.z, nl.w));
-          p1[2 * c4] = sm100::pack_bf16x2(e0.x, e0.y);
-          p1[2 * c4 + 1] = sm100::pack_bf16x2(e1.x, e1.y);
-        }
-        // ---- the previous tile's dQ
-        if (t > 0 && !(ok = drain_dq(tq + t - 1))) break;
-        // ---- P_2, kept in fp32, and W = P_1 - lam P_2
-        if (!(ok = wait(s2_full(h), par, 60))) break;
-        sm100::tc_fence_after();
-        load_s();
-        mask_s();
-        float2 p2[16];
-        uint32_t wv[16];
-#pragma unroll
-        for (int c4 = 0; c4 < 8; ++c4) {
-          const float4 nl = l2v[c4];
-          p2[2 * c4] = prob(2 * c4, make_float2(nl.x, nl.y));
-          p2[2 * c4 + 1] = prob(2 * c4 + 1, make_float2(nl.z, nl.w));
-#pragma unroll
-          for (int e = 2 * c4; e < 2 * c4 + 2; ++e) {
-            const float2 w =
-                __ffma2_rn(p2[e], nlam, f2(p1[e] << 16, p1[e] & 0xFFFF0000u));
-            wv[e] = sm100::pack_bf16x2(w.x, w.y);
-          }
-        }
-        sm100::tmem_st16(s_addr, wv);
-        sm100::tmem_st_wait();
-        arrive(w_full(h));
-        // ---- dS_1 = P_1 (dP - D_1), dS_2 = P_2 (-lam dP + lam D_2): row-contiguous per key,
-        // 16-byte chunk q of line kl_ at q ^ (kl_ & 7)
-        if (!(ok = wait(dp_full(h), par, 62))) break;
-        sm100::tc_fence_after();
-#pragma unroll
-        for (int c16 = 0; c16 < 2; ++c16) {
-          uint32_t dp[16];
-          sm100::tmem_ld16(dp_addr + 16 * c16, dp);
-          sm100::tmem_ld_wait();
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {  // eight columns: one 16-byte chunk of each map
-            uint32_t w1[4], w2[4];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int cc = 4 * c16 + 2 * q + k;  // columns 4 cc ... of the thread's 32
-              const float4 n1 = d1v[cc], n2 = d2v[cc];
-              const float2 nd1[2] = {make_float2(n1.x, n1.y), make_float2(n1.z, n1.w)};
-              const float2 ld2[2] = {make_float2(n2.x, n2.y), make_float2(n2.z, n2.w)};
+            for (int c4 = 0; c4 < 8; ++c4) {
+              const float4 nlse = l1v[c4];
+              const float2 n2[2] = {make_float2(nlse.x, nlse.y), make_float2(nlse.z, nlse.w)};
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int cp = 2 * cc + e;
-                const float2 gp = f2(dp[8 * q + 4 * k + 2 * e], dp[8 * q + 4 * k + 2 * e + 1]);
-                const float2 a =
-                    __fmul2_rn(f2(p1[cp] << 16, p1[cp] & 0xFFFF0000u), __fadd2_rn(gp, nd1[e]));
-                const float2 b = __fmul2_rn(p2[cp], __ffma2_rn(gp, nlam, ld2[e]));
-                lam_acc = __ffma2_rn(p2[cp], gp, lam_acc);
-                w1[2 * k + e] = sm100::pack_bf16x2(a.x, a.y);
-                w2[2 * k + e] = sm100::pack_bf16x2(b.x, b.y);
+                const int cp = 2 * c4 + e;
+                const float2 x = __ffma2_rn(f2(s[2 * cp], s[2 * cp + 1]), sl2, n2[e]);
+                p1[cp] = sm100::pack_bf16x2(sm100::ex2(x.x), sm100::ex2(x.y));
               }
             }
-            const uint32_t at = line + (((4 * (cq & 1) + 2 * c16 + q) ^ (kl_ & 7)) << 4);
-            st_shared_v4(at, w1);
-            st_shared_v4(at + 2 * PANEL, w2);
           }
-        }
-        sm100::fence_proxy_async_smem();
-        arrive(ds_full(h));
-        acc_prev = acc;
-        acc += BMQ * DH;
-        if (++i == i_end) {  // the group's next head
-          float x = lam_acc.x + lam_acc.y;
+          // ---- the previous tile's dQ
+          if ((i > it.i_lo || g > 0) && !(ok = drain_dq(cur - 1))) break;
+          if (i == it.i_lo && g > 0)  // that was the last tile of the head before
+            acc += static_cast<size_t>(p.Lqp - (i_end - it.i_lo) * BMQ) * DH;
+          // ---- sixteen columns at a time: P_2, W = P_1 - lam P_2 (over the dP it goes with),
+          // dS_1 = P_1 (dP - D_1), dS_2 = P_2 (-lam dP + lam D_2), row-contiguous per key,
+          // 16-byte chunk q of line kl_ at q ^ (kl_ & 7)
+          if (!(ok = wait_at(DP_FULL, cur, 62))) break;
+          sm100::tc_fence_after();
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (sm100::lane_id() == 0) lam_part[g * NSMX + warp] = x;
-          lam_acc = make_float2(0.f, 0.f);
-          acc += head_skip;
-          i = it.i_lo;
-          if (++g < p.G && p.n_lam != 1) nl_h = -__ldg(lam + g);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t s[16], dp[16], wv[8];
+            sm100::tmem_ld16(s_addr + 16 * k, s);
+            sm100::tmem_ld16(dp_addr + 16 * k, dp);
+            sm100::tmem_ld_wait();
+            if (k == 1) arrive_at(S2_READ);
+            if (!all_vis) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (16 * k + c < cmin) s[c] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {  // eight columns: one 16-byte chunk of each map
+              uint32_t w1[4], w2[4];
+#pragma unroll
+              for (int c4 = 0; c4 < 2; ++c4) {
+                const int cc = 4 * k + 2 * q + c4;  // columns 4 cc ... of the thread's 32
+                const float4 nl4 = l2v[cc], n1 = d1v[cc], n2 = d2v[cc];
+                const float2 nlse[2] = {make_float2(nl4.x, nl4.y), make_float2(nl4.z, nl4.w)};
+                const float2 nd1[2] = {make_float2(n1.x, n1.y), make_float2(n1.z, n1.w)};
+                const float2 ld2[2] = {make_float2(n2.x, n2.y), make_float2(n2.z, n2.w)};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int j = 8 * q + 4 * c4 + 2 * e;  // of the sixteen columns
+                  const uint32_t u = p1[2 * cc + e];
+                  const float2 pa = f2(u << 16, u & 0xFFFF0000u), gp = f2(dp[j], dp[j + 1]);
+                  const float2 x = __ffma2_rn(f2(s[j], s[j + 1]), sl2, nlse[e]);
+                  const float2 pb = make_float2(sm100::ex2(x.x), sm100::ex2(x.y));
+                  const float2 wf = __ffma2_rn(pb, nlam, pa);
+                  const float2 a = __fmul2_rn(pa, __fadd2_rn(gp, nd1[e]));
+                  const float2 b = __fmul2_rn(pb, __ffma2_rn(gp, nlam, ld2[e]));
+                  lam_acc = __ffma2_rn(pb, gp, lam_acc);
+                  wv[4 * q + 2 * c4 + e] = sm100::pack_bf16x2(wf.x, wf.y);
+                  w1[2 * c4 + e] = sm100::pack_bf16x2(a.x, a.y);
+                  w2[2 * c4 + e] = sm100::pack_bf16x2(b.x, b.y);
+                }
+              }
+              const uint32_t at = line + (((4 * (cq & 1) + 2 * k + q) ^ (kl_ & 7)) << 4);
+              st_shared_v4(at, w1);
+              st_shared_v4(at + 2 * PANEL, w2);
+            }
+            sm100::tmem_st8(dp_addr + 8 * k, wv);
+          }
+          sm100::tmem_st_wait();
+          sm100::fence_proxy_async_smem();
+          arrive_at(DS_FULL);
         }
+        if (!ok) break;
+        float x = lam_acc.x + lam_acc.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0)
+          p.lam_part[((static_cast<size_t>(kvh) * p.n_kv + it.n) * p.G + g) * NSMX + warp] = x;
       }
       if (!ok) break;
-      if (it.T > 0 && !(ok = drain_dq(tq + it.T - 1))) break;
-      tq += it.T;
+      if (it.T > 0 && !(ok = drain_dq(cur - 1))) break;
       // ---------------- epilogue: dV, dK (x scale) of this key row, a quarter of the columns
       if (!(ok = wait(dkv_full, ik & 1, 64))) break;
       sm100::tc_fence_after();
       const bool live = key < p.Lk;
-      const size_t orow = (static_cast<size_t>(it.b) * p.Hkv + it.hkv) * p.Lk + (live ? key : 0);
+      const size_t orow = static_cast<size_t>(kvh) * p.Lk + (live ? key : 0);
       const bool wide =
           ((reinterpret_cast<uintptr_t>(p.dV) | reinterpret_cast<uintptr_t>(p.dK)) & 31) == 0;
       constexpr int DQ = DH / 4;
@@ -805,11 +784,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __nv_bfloat16* dst = (m == 0 ? p.dV : p.dK) + orow * DH + DQ * cq;
         const float f = (m == 0) ? 1.f : p.scale;
         // dK: map 2's half starts 64 columns on (d = 64: its own columns of a full-width product)
-        const uint32_t col = (m == 0 ? DV_COL : DK_COL + (DH == 64 ? 64 * (cq >> 1) : 0)) + DQ * cq;
+        const uint32_t col = s_addr - S_COL - 32 * cq + DQ * cq +
+                             (m == 0 ? DV_COL : DK_COL + (DH == 64 ? 64 * h : 0));
 #pragma unroll 1
         for (int c = 0; c < DQ; c += 16) {
           uint32_t v[16], o[8];
-          sm100::tmem_ld16(tmem + lane_base + col + c, v);
+          sm100::tmem_ld16(col + c, v);
           sm100::tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -827,7 +807,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
       }
-      arrive(dkv_empty);
+      sm100::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(dkv_empty);
     }
   }
 
