@@ -18,7 +18,8 @@
 //                               is issued)
 //   dP^T = V dO^T              (SS, 64 columns)
 //   dV  += W^T dO              (TS, W = P_1 - lam P_2 in bf16 over the dP columns)
-//   dK_m += dS_m^T Q_m         (SS, N = 64, dS_m staged in shared memory)
+//   dK_m += dS_m^T Q_m         (N = 64, dS_m staged in shared memory; dS_1 is also put beside
+//                               W over the dP columns, so that dK_1 reads it there: TS)
 //   dQ_m^T = K_m^T dS_m^T      (SS, M = 64, lanes = head dimension, over the dP columns:
 //                               map 1 in lanes 0-15 of each 32, map 2 in lanes 16-31)
 // dV (d columns) and dK (64 per map) stay in TMEM for the item: 512 columns in all.
@@ -40,7 +41,10 @@
 //
 // Measured on B200 (causal B2 H16 L8192 d128): dQ staged in the dS buffers and one tile
 // at a time 2715 us; dQ by reductions 2392; halves in turn 2031; fewer waits and no
-// divisions 1869; P_2 and dS in one go 1701.
+// divisions 1869; P_2 and dS in one go 1672; dK_1 by TS 1637.  What bounds it now is
+// shared memory: the products read 416 KB of operands per 128-row tile (an SS product at
+// N = 64 is fed at ~95 of the 128 bytes a cycle), the copies in, the dS and the statistics'
+// broadcasts take another 190 KB, about 4700 of the ~6300 cycles of a tile.
 //
 // dlam needs more of P_2 than bf16 gives: its terms P_2 dP have both signs, and
 // the roundings of P_2 (2^-9 relative on average) do not shrink with the sum.
@@ -481,12 +485,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
     };
-    auto issue_dv = [&](int h, bool first) {  // W: a warp's 32 rows are 16 columns
+    auto issue_dv = [&](int h, bool first) {  // W: sixteen rows are 8 of every 16 columns
       const uint64_t bd = sm100::sdesc_sw128(doA + h * HROWS, PANEL, 1024);
       if (leader) {
 #pragma unroll
         for (int k = 0; k < HQ / 16; ++k)
-          sm100::mma_ts(tmem + DV_COL, tmem + DP_COL + HQ * h + (k >> 1) * 32 + (k & 1) * 8,
+          sm100::mma_ts(tmem + DV_COL, tmem + DP_COL + HQ * h + 16 * k,
                         bd + ((k * 2048) >> 4), C::IDESC_DV, (!first || k > 0) ? 1u : 0u);
       }
     };
@@ -502,6 +506,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int k = 0; k < HQ / 16; ++k)
           sm100::mma_ss(tmem + DK_COL + 64 * m, ad + 2 * k, bd + ((k * 2048) >> 4), IDESC_DK,
                         (!first || k > 0) ? 1u : 0u);
+      }
+    };
+    auto issue_dk1_ts = [&](uint32_t tile, int h, bool first) {  // dS_1 from the dP columns
+      const uint64_t bd = sm100::sdesc_sw128(qA(tile) + h * HROWS, PANEL, 1024);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < HQ / 16; ++k)
+          sm100::mma_ts(tmem + DK_COL, tmem + DP_COL + HQ * h + 16 * k + 8, bd + ((k * 2048) >> 4),
+                        IDESC_DK, (!first || k > 0) ? 1u : 0u);
       }
     };
     auto issue_dq = [&](int h, int m) {
@@ -555,6 +568,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         sm100::tc_fence_after();
         issue_dv(h, first);
         commit(do_empty(h));
+        issue_dk1_ts(tq + t, h, first);
         issue_dq(h, 0);
         issue_dq(h, 1);
         commit(dq_full(h));
@@ -562,7 +576,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       };
       auto both_dk = [&](int t, int h) {
         const bool first = t == 0 && h == 0;
-        issue_dk(tq + t, h, 0, first);
         issue_dk(tq + t, h, 1, first);
         commit(q_empty(h, tq + t));
       };
@@ -716,7 +729,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           sm100::tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            uint32_t s[16], dp[16], wv[8];
+            uint32_t s[16], dp[16], wv[16];  // wv: W, then dS_1, eight words each
             sm100::tmem_ld16(s_addr + 16 * k, s);
             sm100::tmem_ld16(dp_addr + 16 * k, dp);
             sm100::tmem_ld_wait();
@@ -753,10 +766,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
               }
               const uint32_t at = line + (((4 * (cq & 1) + 2 * k + q) ^ (kl_ & 7)) << 4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) wv[8 + 4 * q + e] = w1[e];
               st_shared_v4(at, w1);
               st_shared_v4(at + 2 * PANEL, w2);
             }
-            sm100::tmem_st8(dp_addr + 8 * k, wv);
+            sm100::tmem_st16(dp_addr + 16 * k, wv);
           }
           sm100::tmem_st_wait();
           sm100::fence_proxy_async_smem();
