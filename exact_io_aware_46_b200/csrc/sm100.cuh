@@ -362,6 +362,26 @@ __device__ __forceinline__ float2 ex2_poly2(float2 x_in) {
   return make_float2(x_in.x < -125.f ? 0.f : rx, x_in.y < -125.f ? 0.f : ry);
 }
 
+// The same with a degree-4 polynomial (2.79e-6, from exp2_poly_fit.py 4), for sums that are
+// kept as a statistic, and without the zeroing of inputs below -125: those (-inf
+// included) give about 2^-126, so the caller must know a row without any other
+// entry by its maximum.
+__device__ __forceinline__ float2 ex2_poly4_nz(float2 x) {
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  const float2 magic = make_float2(12582912.f, 12582912.f);
+  const float2 t = __fadd2_rn(x, magic);
+  const float2 n = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
+  const float2 f = __fadd2_rn(x, make_float2(-n.x, -n.y));
+  float2 q = __ffma2_rn(make_float2(0.009584325f, 0.009584325f), f,
+                        make_float2(0.05590752f, 0.05590752f));
+  q = __ffma2_rn(q, f, make_float2(0.24024066f, 0.24024066f));
+  q = __ffma2_rn(q, f, make_float2(0.693124f, 0.693124f));
+  q = __ffma2_rn(q, f, make_float2(1.f, 1.f));
+  return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
+}
+
 // Two fp32 -> packed bf16x2 (round to nearest even); `lo` lands in bits 0-15.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;

@@ -193,3 +193,30 @@ def test_fwd_rejects_on_host():
     assert call(d=96) == attn.ATTN_ERR_UNSUPPORTED
     assert call(B=1 << 20, Lq=1 << 20) == attn.ATTN_ERR_UNSUPPORTED
     assert call(Lq=0) == 0 and call(Lq=0, Q=None, O=None) == 0
+
+
+def test_polynomial_exponential():
+    """The differential forward's software 2^x: degree 4, within 2.9e-6 of the exact value, read
+    from the CUDA source; the fit reproduces its constants."""
+    import os
+    import re
+    import sys
+
+    import numpy as np
+
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                        "exact_io_aware_46_b200", "csrc")
+    src = open(os.path.join(csrc, "sm100.cuh")).read()
+    body = src[src.index("ex2_poly4_nz(float2 x)"):]
+    body = body[:body.index("\n}\n")]
+    pairs = re.findall(r"make_float2\(([0-9.e-]+)f, \1f\)", body)
+    coef = [float(v) for v in pairs if abs(float(v)) < 100][::-1]  # c0 ... c4
+    assert len(coef) == 5 and coef[0] == 1.0
+    sys.path.insert(0, csrc)
+    from exp2_poly_fit import eval_f32, fit
+
+    x = np.linspace(-125.0, 8.0, 2_000_001, dtype=np.float32)
+    y = eval_f32(coef, x).astype(np.float64)
+    assert np.abs(y / np.exp2(x.astype(np.float64)) - 1.0).max() <= 2.9e-6
+    want, err = fit(4)
+    assert err <= 2.8e-6 and np.allclose(np.float32(coef), np.float32(want), rtol=1e-5)
