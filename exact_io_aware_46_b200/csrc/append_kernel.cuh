@@ -11,10 +11,11 @@
 // caller's; products and sums are fp32, rounded once to bf16.  V is copied.
 //
 // HBM-bound: each element is read once and written once.  A head row is D / 16
-// units of 16 elements -- a rotated unit is eight pairs, i.e. two 16-byte chunks
-// rope / 2 apart (or 32 contiguous bytes) -- and a thread keeps its unit while it
-// walks the token's head rows, so the 16 fp32 angles' cosines and sines are read
-// once per token and unit instead of once per row (twice the row's own bytes).
+// units of two 16-byte chunks, chosen so that neighbouring lanes hold neighbouring
+// chunks (64 to 128 bytes a run) in either pairing: a rotated unit of the split
+// pairing is the two chunks that rotate into each other, rope / 2 apart.  A thread
+// keeps its unit while it walks the token's head rows, so its 16 fp32 cosines and
+// sines are read once per token instead of once per row (twice the row's own bytes).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,7 +41,10 @@ struct Params {
   int rows_per_y;  // head rows (Q, then K, then V) of a token that one block walks
 };
 
-constexpr int NTHREADS = 256;
+// Small blocks: a block's index loads are a chain (offsets, length, block table), which others
+// cover.  Measured on B200 (40,897 packed tokens, Hq = Hkv = 16, d = 128, interleaved, 1.0 GB):
+// 256 threads 213 us, 128 172 us, 64 167 us (6.0 TB/s; a copy of as many bytes 156 us).
+constexpr int NTHREADS = 64;
 constexpr int BAD_KLEN = 1, BAD_PAGE = 4;  // device status bits
 
 // The sequence that token t belongs to: the number of sequences ending at or
@@ -59,6 +63,16 @@ __device__ __forceinline__ int find_sequence(const int* cu, int B, int t) {
   return lo;
 }
 
+// Sixteen bytes that nothing else will read; not the read-only path, since Q may be
+// rotated in place.
+__device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 template <int D>
 __global__ void __launch_bounds__(NTHREADS) append_kernel(const Params p) {
   constexpr int UPR = D / 16;               // units per head row
@@ -68,13 +82,24 @@ __global__ void __launch_bounds__(NTHREADS) append_kernel(const Params p) {
   const int row_end = min((static_cast<int>(blockIdx.y) + 1) * p.rows_per_y, p.q_rows + 2 * p.Hkv);
   int row = blockIdx.y * p.rows_per_y + threadIdx.x / UPR;
 
-  // this thread's unit: element offsets of its two chunks and its first angle
-  const int part = D / p.maps;
-  const int m = u / (part / 16), w = u % (part / 16);
-  const bool rot = w < p.rope / 16;
-  const bool split = rot && !p.interleaved;
-  const int a_off = m * part + (split ? 8 : 16) * w;
-  const int b_off = a_off + (split ? p.rope / 2 : 8);
+  // this thread's unit: its two chunks, of its part's pc chunks (rc of them rotated)
+  const int part = D / p.maps, pc = part / 8, rc = p.rope / 8;
+  const int m = u / (pc / 2), w = u % (pc / 2);
+  int ca, cb;         // chunks within the part
+  bool rot_a, rot_b;  // rotated
+  if (p.interleaved || w >= rc / 2) {
+    // pairs lie within a chunk, or nothing is rotated: chunks half the range apart
+    const int lo = p.interleaved ? 0 : rc, half = (pc - lo) / 2;
+    ca = lo + w - (p.interleaved ? 0 : rc / 2);
+    cb = ca + half;
+    rot_a = ca < rc;
+    rot_b = cb < rc;
+  } else {
+    ca = w;
+    cb = w + rc / 2;
+    rot_a = rot_b = true;
+  }
+  const int a_off = m * part + 8 * ca, b_off = m * part + 8 * cb;
 
   auto source = [&](int r) -> const __nv_bfloat16* {
     if (r < p.q_rows) return p.Q + t * p.q_stride + static_cast<long long>(r) * D;
@@ -86,8 +111,8 @@ __global__ void __launch_bounds__(NTHREADS) append_kernel(const Params p) {
   uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
   if (row < row_end) {
     const __nv_bfloat16* s = source(row);
-    a = *reinterpret_cast<const uint4*>(s + a_off);
-    b = *reinterpret_cast<const uint4*>(s + b_off);
+    a = load_once(s + a_off);
+    b = load_once(s + b_off);
   }
 
   // sequence, cache row and page of the token (uniform over the block)
@@ -117,13 +142,18 @@ __global__ void __launch_bounds__(NTHREADS) append_kernel(const Params p) {
     if (!ok && threadIdx.x == 0) atomicOr(p.status, BAD_PAGE);
   }
   if (ok) {
+    // four angles of each chunk's pairs (interleaved), or the eight that both share
     float c[8], s[8];
-    if (rot) {
-      const size_t at = static_cast<size_t>(r) * (p.rope / 2) + 8 * w;
+    if (rot_a || rot_b) {
+      const size_t row_at = static_cast<size_t>(r) * (p.rope / 2);
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos_t + at) + v);
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(p.sin_t + at) + v);
+        const int first4 = p.interleaved ? 4 * (v ? cb : ca) : 8 * ca + 4 * v;
+        float4 cv = make_float4(1.f, 1.f, 1.f, 1.f), sv = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (v ? rot_b : rot_a) {
+          cv = __ldg(reinterpret_cast<const float4*>(p.cos_t + row_at + first4));
+          sv = __ldg(reinterpret_cast<const float4*>(p.sin_t + row_at + first4));
+        }
         c[4 * v] = cv.x; c[4 * v + 1] = cv.y; c[4 * v + 2] = cv.z; c[4 * v + 3] = cv.w;
         s[4 * v] = sv.x; s[4 * v + 1] = sv.y; s[4 * v + 2] = sv.z; s[4 * v + 3] = sv.w;
       }
@@ -131,14 +161,15 @@ __global__ void __launch_bounds__(NTHREADS) append_kernel(const Params p) {
     const int in_page = r & ((1 << p.page_log2) - 1);
     while (row < row_end) {
       __nv_bfloat16* dst;
-      bool turn = rot;
+      bool turn_a = rot_a, turn_b = rot_b;
       if (row < p.q_rows) {
         dst = p.Q_out + (static_cast<size_t>(t) * p.Hq + row) * D;
       } else {
         int h = row - p.q_rows;
         const bool is_v = h >= p.Hkv;
         if (is_v) h -= p.Hkv;
-        turn = rot && !is_v;
+        turn_a = rot_a && !is_v;
+        turn_b = rot_b && !is_v;
         dst = (is_v ? p.Vp : p.Kp) +
               (((static_cast<size_t>(pg) * p.Hkv + h) << p.page_log2) + in_page) * D;
       }
@@ -146,10 +177,10 @@ __global__ void __launch_bounds__(NTHREADS) append_kernel(const Params p) {
       uint4 na = a, nb = b;
       if (next < row_end) {  // the next row's data before this row's arithmetic
         const __nv_bfloat16* sp = source(next);
-        na = *reinterpret_cast<const uint4*>(sp + a_off);
-        nb = *reinterpret_cast<const uint4*>(sp + b_off);
+        na = load_once(sp + a_off);
+        nb = load_once(sp + b_off);
       }
-      if (turn) {
+      if (turn_a || turn_b) {
         uint32_t* av = reinterpret_cast<uint32_t*>(&a);
         uint32_t* bv = reinterpret_cast<uint32_t*>(&b);
         auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
@@ -158,9 +189,10 @@ __global__ void __launch_bounds__(NTHREADS) append_kernel(const Params p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float xa = lo(av[e]), ya = hi(av[e]), xb = lo(bv[e]), yb = hi(bv[e]);
-            av[e] = sm100::pack_bf16x2(xa * c[e] - ya * s[e], ya * c[e] + xa * s[e]);
-            bv[e] = sm100::pack_bf16x2(xb * c[4 + e] - yb * s[4 + e],
-                                       yb * c[4 + e] + xb * s[4 + e]);
+            if (turn_a) av[e] = sm100::pack_bf16x2(xa * c[e] - ya * s[e], ya * c[e] + xa * s[e]);
+            if (turn_b)
+              bv[e] = sm100::pack_bf16x2(xb * c[4 + e] - yb * s[4 + e],
+                                         yb * c[4 + e] + xb * s[4 + e]);
           }
         } else {  // element e of the first chunk pairs with element e of the second
 #pragma unroll
