@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* red = reinterpret_cast<float*>(smem + OFF_RED);
 
+  if constexpr (DIFF) sm100::grid_launch_dependents();  // the combine's set-up
   // grid (sequence x kv head, chunk position counted from the sequence's end)
   const int hkv = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
   const int kl = valid_klen(p.k_lens, b, p.Lmax, p.status,
@@ -532,13 +533,16 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const CombineParams p
 
 // ---------------------------------------------------------------- differential decode
 
-// Keys per split: the longest of 2048, 1024, 512 and 256 that still gives every
-// SM two chunks of the cache's capacity (the lengths are on the device), since a
-// short grid leaves SMs without a stream of their own.
+// Keys per split: the longest of 2048, 1024, ..., 128 that still gives every SM a split
+// of the cache's capacity (the lengths are on the device), since a short grid leaves
+// SMs without a stream of their own, and a longer one only adds set-up and partials.
+// Measured on B200 (splits for 148 / 296 of them at least, us): B1 Hkv1 d128 cache 131072
+// 27.5 / 42.2, B1 Hkv8 32768 30.7 / 35.8, B16 Hkv8 4096 40.7 / 48.4, B7 Hkv2 d64 9001
+// 19.0 / 19.7; a lower limit of 128 instead of 256 keys: B1 Hkv8 512 9.4 / 10.4.
 inline int diff_chunk(int B, int Hkv, int Lmax) {
-  const long long want = 2 * 148;
+  const long long want = 148;
   int ch = CH;
-  while (ch > 256 && static_cast<long long>(B) * Hkv * ((Lmax + ch - 1LL) / ch) < want) ch /= 2;
+  while (ch > 128 && static_cast<long long>(B) * Hkv * ((Lmax + ch - 1LL) / ch) < want) ch /= 2;
   return ch;
 }
 
@@ -563,66 +567,83 @@ struct DiffCombineParams {
 };
 
 // Joins both maps' partials (the normalised rule of decode_combine_kernel, per
-// map) and subtracts: O = O_1 - lam O_2.  One block per (sequence, query head),
-// a warp per chunk in turn, each lane D / 32 columns of both maps.
+// map) and subtracts: O = O_1 - lam O_2.  One block per (sequence, query head), even
+// warps for the first map and odd ones for the second, four splits of a map at a time,
+// each lane D / 32 columns.  The length, the log-sum-exps and the first partials are
+// requested together: a row past the length is dropped by selection.
 constexpr int DC_WARPS = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * DC_WARPS) diff_combine_kernel(const DiffCombineParams p) {
   constexpr int EPL = D / 32;
-  __shared__ float acc_s[DC_WARPS][2][D];
+  __shared__ float acc_s[DC_WARPS][D];
+  __shared__ float wsum_s[2];
   const int bh = blockIdx.x, b = bh / p.Hq, h = bh % p.Hq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m = warp & 1;
+  const float* lp = p.part_lse + (static_cast<size_t>(bh) * 2 + m) * p.nsm;
+  const float* op = p.part_o + (static_cast<size_t>(bh) * 2 + m) * p.nsm * D + lane * EPL;
+  const float lam = __ldg(p.lam + (p.n_lam == 1 ? 0 : h));
   int kl = __ldg(p.k_lens + b);
+  sm100::grid_wait();
   if (kl < 0 || kl > p.Lmax) kl = 0;  // reported by the split kernel
   const int n = (kl + p.ch - 1) / p.ch;
-  float M[2], wsum[2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float* lp = p.part_lse + (static_cast<size_t>(bh) * 2 + m) * p.nsm;
-    float x = -INFINITY;
-    for (int c = lane; c < n; c += 32) x = fmaxf(x, lp[c]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    M[m] = x;
-    float ws = 0.f;  // every warp sums all weights: the same value in each
-    for (int c = lane; c < n; c += 32) ws += lp[c] == -INFINITY ? 0.f : sm100::ex2(lp[c] - x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-    wsum[m] = ws;
-    float acc[EPL] = {};
-    const float* op = p.part_o + (static_cast<size_t>(bh) * 2 + m) * p.nsm * D + lane * EPL;
-    for (int c = warp; c < n; c += DC_WARPS) {
-      const float w = lp[c] == -INFINITY ? 0.f : sm100::ex2(lp[c] - x);
-      const float* src = op + static_cast<size_t>(c) * D;
-      if constexpr (EPL == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] += w * v.x; acc[1] += w * v.y; acc[2] += w * v.z; acc[3] += w * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] += w * v.x; acc[1] += w * v.y;
-      }
+  auto load = [&](int c, float (&v)[EPL]) {
+    const float* src = op + static_cast<size_t>(c) * D;
+    if constexpr (EPL == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(src);
+      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+    } else {
+      const float2 t = *reinterpret_cast<const float2*>(src);
+      v[0] = t.x; v[1] = t.y;
     }
+  };
+  // a block of 32 splits at a time: the warp's eight of them at once
+  constexpr int STEP = DC_WARPS / 2, PER = 32 / STEP;
+  const int c0 = warp >> 1;
+  float v[PER][EPL];
+  auto load_block = [&](int base, int end) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc_s[warp][m][lane * EPL + e] = acc[e];
+    for (int k = 0; k < PER; ++k)
+      if (base + c0 + k * STEP < end) load(base + c0 + k * STEP, v[k]);
+  };
+  load_block(0, p.nsm);
+  const float l0 = lane < p.nsm ? lp[lane] : -INFINITY;  // the first 32 splits
+  float M = lane < n ? l0 : -INFINITY;
+  for (int c = lane + 32; c < n; c += 32) M = fmaxf(M, lp[c]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float ws = 0.f, acc[EPL] = {};
+  for (int base = 0; base < n; base += 32) {
+    const float l = base == 0 ? l0 : base + lane < n ? lp[base + lane] : -INFINITY;
+    const float w = (base + lane < n && l != -INFINITY) ? sm100::ex2(l - M) : 0.f;
+    ws += w;
+    if (base > 0) load_block(base, n);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const float wc = __shfl_sync(0xffffffffu, w, c0 + k * STEP);
+      if (base + c0 + k * STEP < n)
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[e] += wc * v[k][e];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) acc_s[warp][lane * EPL + e] = acc[e];
+  if (warp < 2 && lane == 0) {
+    wsum_s[m] = ws;
+    if (p.lse)
+      p.lse[static_cast<size_t>(bh) * 2 + m] =
+          ws > 0.f ? (M + log2f(ws)) * 0.69314718055994531f : -INFINITY;
   }
   __syncthreads();
   if (threadIdx.x < D) {
     float o[2] = {0.f, 0.f};
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-      if (wsum[m] > 0.f) {
-#pragma unroll
-        for (int k = 0; k < DC_WARPS; ++k) o[m] += acc_s[k][m][threadIdx.x];
-        o[m] /= wsum[m];
-      }
-    const float lam = __ldg(p.lam + (p.n_lam == 1 ? 0 : h));
-    p.O[static_cast<size_t>(bh) * D + threadIdx.x] =
-        __float2bfloat16_rn(wsum[0] > 0.f ? o[0] - lam * o[1] : 0.f);
-  }
-  if (p.lse && threadIdx.x < 2) {
-    const float ws = threadIdx.x ? wsum[1] : wsum[0], mx = threadIdx.x ? M[1] : M[0];
-    p.lse[static_cast<size_t>(bh) * 2 + threadIdx.x] =
-        ws > 0.f ? (mx + log2f(ws)) * 0.69314718055994531f : -INFINITY;
+    for (int k = 0; k < DC_WARPS; ++k) o[k & 1] += acc_s[k][threadIdx.x];
+    // (a map without a key has a sum of zero; both maps see the same keys)
+    p.O[static_cast<size_t>(bh) * D + threadIdx.x] = __float2bfloat16_rn(
+        wsum_s[0] > 0.f && wsum_s[1] > 0.f ? o[0] / wsum_s[0] - lam * (o[1] / wsum_s[1]) : 0.f);
   }
 }
 
@@ -720,8 +741,10 @@ cudaError_t launch_diff_d(const SplitParams& sp, const DiffCombineParams& cp, bo
   const cudaError_t e =
       paged ? launch_split<D, true, true>(sp, s) : launch_split<D, false, true>(sp, s);
   if (e != cudaSuccess) return e;
-  diff_combine_kernel<D><<<sp.B * sp.Hq, 32 * DC_WARPS, 0, s>>>(cp);
-  return attn_host::report_launch(diff_combine_kernel<D>, "diff_combine_kernel");
+  return attn_host::report(
+      attn_host::launch_overlapped(diff_combine_kernel<D>, dim3(sp.B * sp.Hq), dim3(32 * DC_WARPS),
+                                   0, s, cp),
+      "diff_combine_kernel");
 }
 
 // Differential decode: lam [n_lam] (one weight, or one per query head), lse [B*Hq][2].

@@ -160,44 +160,43 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, const uint32_t (&w)[4]
 
 // ------------------------------------------------------------------ prep
 
-// One warp per (padded) query row: D_1, D_2, the log2-LSEs and a zeroed accumulator row.
+// D_1, D_2, the log2-LSEs and a zeroed accumulator row of every (padded) query row: DH / 8
+// lanes a row, sixteen bytes each of O, O2 and dO.
 template <int DH>
 __global__ void __launch_bounds__(256)
     prep_kernel(const __nv_bfloat16* O, const __nv_bfloat16* O2, const __nv_bfloat16* dO,
                 const float* lse, const float* lam, int n_lam, float* dq_acc, float* stats,
                 long long rows, int Hq, int Lq, int Lqp) {
-  constexpr int EPL = DH / 32;
-  const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
+  constexpr int LPR = DH / 8;  // lanes per row
+  sm100::grid_launch_dependents();
+  const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+  const int lane = threadIdx.x % LPR;
+  if (row >= rows) return;  // whole rows, and rows is a multiple of 128: whole warps
   const long long bh = row / Lqp;
-  const int r = static_cast<int>(row % Lqp);
+  const int r = static_cast<int>(row - bh * Lqp);
   float a1 = 0.f, a2 = 0.f;
   if (r < Lq) {
-    const size_t off = (static_cast<size_t>(bh) * Lq + r) * DH + lane * EPL;
-    uint32_t o[EPL / 2], o2[EPL / 2], g[EPL / 2];
+    const size_t off = (static_cast<size_t>(bh) * Lq + r) * DH + lane * 8;
+    const uint4 o = __ldg(reinterpret_cast<const uint4*>(O + off));
+    const uint4 o2 = __ldg(reinterpret_cast<const uint4*>(O2 + off));
+    const uint4 g = __ldg(reinterpret_cast<const uint4*>(dO + off));
+    const uint32_t ov[4] = {o.x, o.y, o.z, o.w}, o2v[4] = {o2.x, o2.y, o2.z, o2.w};
+    const uint32_t gv[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-    for (int e = 0; e < EPL / 2; ++e) {
-      o[e] = reinterpret_cast<const uint32_t*>(O + off)[e];
-      o2[e] = reinterpret_cast<const uint32_t*>(O2 + off)[e];
-      g[e] = reinterpret_cast<const uint32_t*>(dO + off)[e];
-    }
-#pragma unroll
-    for (int e = 0; e < EPL / 2; ++e) {
-      const float g0 = __uint_as_float(g[e] << 16), g1 = __uint_as_float(g[e] & 0xFFFF0000u);
-      a1 += __uint_as_float(o[e] << 16) * g0 + __uint_as_float(o[e] & 0xFFFF0000u) * g1;
-      a2 += __uint_as_float(o2[e] << 16) * g0 + __uint_as_float(o2[e] & 0xFFFF0000u) * g1;
+    for (int e = 0; e < 4; ++e) {
+      const float g0 = __uint_as_float(gv[e] << 16), g1 = __uint_as_float(gv[e] & 0xFFFF0000u);
+      a1 += __uint_as_float(ov[e] << 16) * g0 + __uint_as_float(ov[e] & 0xFFFF0000u) * g1;
+      a2 += __uint_as_float(o2v[e] << 16) * g0 + __uint_as_float(o2v[e] & 0xFFFF0000u) * g1;
     }
   }
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
+  for (int o = LPR / 2; o >= 1; o >>= 1) {
     a1 += __shfl_xor_sync(0xffffffffu, a1, o);
     a2 += __shfl_xor_sync(0xffffffffu, a2, o);
   }
-  float* zrow = dq_acc + static_cast<size_t>(row) * DH + lane * EPL;
-#pragma unroll
-  for (int e = 0; e < EPL; e += 2)
-    *reinterpret_cast<float2*>(zrow + e) = make_float2(0.f, 0.f);
+  float4* zrow = reinterpret_cast<float4*>(dq_acc + static_cast<size_t>(row) * DH);
+  zrow[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+  zrow[lane + LPR] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (lane < 4) {
     const int h = static_cast<int>(bh % Hq);
     const float l = __ldg(lam + (n_lam == 1 ? 0 : h));
@@ -213,26 +212,30 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// dQ = bf16(scale * accumulator), four elements a thread; the blocks behind those that
+// dQ = bf16(scale * accumulator), eight elements a thread; the blocks behind those that
 // convert add up dlam (one block per weight), each warp's sums in a fixed order.
 template <int DH>
 __global__ void __launch_bounds__(256)
     finish_kernel(const float* dq_acc, __nv_bfloat16* dQ, long long BH, int Lq, int Lqp,
                   float scale, long long conv_blocks, const float* lam_part, __nv_bfloat16* dlam,
                   int B, int Hq, int Hkv, int n_kv, int n_lam) {
+  sm100::grid_wait();
   if (blockIdx.x < conv_blocks) {
     const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const size_t total = static_cast<size_t>(BH) * Lq * (DH / 4);
+    const size_t total = static_cast<size_t>(BH) * Lq * (DH / 8);
     if (i >= total) return;
-    const size_t row = i / (DH / 4);
-    const int c4 = static_cast<int>(i % (DH / 4));
-    const size_t bh = row / Lq, r = row % Lq;
-    const float4 v = *reinterpret_cast<const float4*>(dq_acc + (bh * Lqp + r) * DH +
-                                                      acc_pos<DH>(4 * c4));
-    uint2 o;
-    o.x = sm100::pack_bf16x2(v.x * scale, v.y * scale);
-    o.y = sm100::pack_bf16x2(v.z * scale, v.w * scale);
-    reinterpret_cast<uint2*>(dQ + row * DH)[c4] = o;
+    const size_t row = i / (DH / 8);
+    const int c8 = static_cast<int>(i % (DH / 8));
+    const size_t bh = row / Lq, r = row - bh * Lq;
+    const float4* src =
+        reinterpret_cast<const float4*>(dq_acc + (bh * Lqp + r) * DH + acc_pos<DH>(8 * c8));
+    const float4 u = src[0], v = src[1];
+    uint4 o;
+    o.x = sm100::pack_bf16x2(u.x * scale, u.y * scale);
+    o.y = sm100::pack_bf16x2(u.z * scale, u.w * scale);
+    o.z = sm100::pack_bf16x2(v.x * scale, v.y * scale);
+    o.w = sm100::pack_bf16x2(v.z * scale, v.w * scale);
+    reinterpret_cast<uint4*>(dQ + row * DH)[c8] = o;
     return;
   }
   const int w = static_cast<int>(blockIdx.x - conv_blocks);
@@ -348,6 +351,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     sm100::tmem_alloc(tmem_slot, 512);
     sm100::tmem_relinquish();
   }
+  // the set-up so far ran beside the preparation's end; its statistics and zeroes are used from here
+  sm100::grid_wait();
+  sm100::grid_launch_dependents();
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
@@ -902,7 +908,7 @@ attn_status_t launch_d(const Args& a, cudaStream_t s) {
 
   if (a.Lq > 0) {
     const long long rows = BH * p.Lqp;
-    prep_kernel<DH><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(
+    prep_kernel<DH><<<static_cast<unsigned>((rows * (DH / 8) + 255) / 256), 256, 0, s>>>(
         a.O, a.O2, a.dO, a.lse, a.lam, a.n_lam, p.dq_acc, stats, rows, a.Hq, a.Lq, p.Lqp);
     if (attn_host::report_launch(prep_kernel<DH>, "diff prep_kernel") != cudaSuccess)
       return ATTN_ERR_CUDA;
@@ -924,15 +930,18 @@ attn_status_t launch_d(const Args& a, cudaStream_t s) {
                           "diff main_kernel shared-memory attribute") != cudaSuccess)
       return ATTN_ERR_CUDA;
     const int grid = p.n_items < a.sms ? p.n_items : a.sms;
-    main_kernel<DH><<<grid, NTHREADS, C::SMEM_BYTES, s>>>(tq, tdo, tk, tv, p);
-    if (attn_host::report_launch(main_kernel<DH>, "diff main_kernel") != cudaSuccess)
+    if (attn_host::report(attn_host::launch_overlapped(main_kernel<DH>, dim3(grid), dim3(NTHREADS),
+                                                       C::SMEM_BYTES, s, tq, tdo, tk, tv, p),
+                          "diff main_kernel") != cudaSuccess)
       return ATTN_ERR_CUDA;
   }
-  const long long conv = (BH * a.Lq * (DH / 4) + 255) / 256;
-  finish_kernel<DH><<<static_cast<unsigned>(conv + a.n_lam), 256, 0, s>>>(
-      p.dq_acc, a.dQ, BH, a.Lq, p.Lqp, a.scale, conv, p.lam_part, a.dlam, a.B, a.Hq, a.Hkv, p.n_kv,
-      a.n_lam);
-  return attn_host::report_launch(finish_kernel<DH>, "diff finish_kernel") == cudaSuccess
+  const long long conv = (BH * a.Lq * (DH / 8) + 255) / 256;
+  return attn_host::report(
+             attn_host::launch_overlapped(finish_kernel<DH>, dim3(static_cast<unsigned>(conv + a.n_lam)),
+                                          dim3(256), 0, s, p.dq_acc, a.dQ, BH, a.Lq, p.Lqp, a.scale,
+                                          conv, p.lam_part, a.dlam, a.B, a.Hq, a.Hkv, p.n_kv,
+                                          a.n_lam),
+             "diff finish_kernel") == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_CUDA;
 }

@@ -100,4 +100,23 @@ cudaError_t report_launch(K kernel, const char* where) {
   return e;
 }
 
+// Launches `kernel` so that it may start while the kernel before it on the stream still
+// runs (programmatic dependent launch): its set-up then overlaps that kernel's end.  It
+// must execute griddepcontrol.wait before it touches anything that kernel writes.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 }  // namespace attn_host
