@@ -772,7 +772,7 @@ attn_status_t attn_bwd_sliding(const attn_bf16_t* Q, const attn_bf16_t* K, const
 
 size_t attn_bwd_diff_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk, int d) {
   if (!shapes_ok(B, Hq, Hkv, Lq, Lk) || d < 0) return kStatusBytes;
-  return kStatusBytes + attn_diff_bwd_impl::scratch(B, Hq, Lq, Lk, d).total;
+  return kStatusBytes + attn_diff_bwd_impl::scratch_bytes(B, Hq, Hkv, Lq, Lk, d);
 }
 
 attn_status_t attn_bwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const attn_bf16_t* V,

@@ -54,6 +54,7 @@
 #pragma once
 
 #include <climits>
+#include <cmath>
 
 #include "bwd_kernel.cuh"
 
@@ -120,8 +121,24 @@ struct Params : attn_bwd_impl::Params {
   const float* stats;  // [B*Hq][n_qt][2 halves][4][64]: -lse2_1, -lse2_2, -D_1, lam D_2
   const float* lam;    // [n_lam]
   int n_lam;
-  float* lam_part;  // [n_items][G][NSMX] sums of P_2 dP
+  float* lam_part;  // [B*Hkv][n_kv][n_split][G][NSMX] sums of P_2 dP
+  int n_split;      // parts that an item's query tiles are shared out to
+  float* kv_part;   // n_split > 1: [n_split][B*Hkv*Lk][dV, dK][d] fp32
 };
+
+// Part `part` of an item: its query tiles t0 ... t0 + T - 1.
+struct Part {
+  Item it;
+  int part, t0, T;
+};
+__device__ __forceinline__ Part get_part(const Params& p, int w, bool* bad) {
+  Part q;
+  q.it = get_item(p, w / p.n_split, bad);
+  q.part = w % p.n_split;
+  q.t0 = static_cast<int>(static_cast<long long>(q.it.T) * q.part / p.n_split);
+  q.T = static_cast<int>(static_cast<long long>(q.it.T) * (q.part + 1) / p.n_split) - q.t0;
+  return q;
+}
 
 // sm100::mbar_wait with the slow path out of line and a longer suspension per try: the
 // waiting warps' polls otherwise take issue slots and shared-memory accesses from the others.
@@ -213,13 +230,40 @@ __global__ void __launch_bounds__(256)
 }
 
 // dQ = bf16(scale * accumulator), eight elements a thread; the blocks behind those that
-// convert add up dlam (one block per weight), each warp's sums in a fixed order.
+// convert add up dlam (one block per weight), each warp's sums in a fixed order, and the
+// parts' dV and dK where an item was split.
 template <int DH>
 __global__ void __launch_bounds__(256)
     finish_kernel(const float* dq_acc, __nv_bfloat16* dQ, long long BH, int Lq, int Lqp,
                   float scale, long long conv_blocks, const float* lam_part, __nv_bfloat16* dlam,
-                  int B, int Hq, int Hkv, int n_kv, int n_lam) {
+                  int B, int Hq, int Hkv, int Lk, int n_lam, int n_split, const float* kv_part,
+                  __nv_bfloat16* dK, __nv_bfloat16* dV) {
   sm100::grid_wait();
+  const int n_kv = (Lk + BN - 1) / BN;
+  if (blockIdx.x >= conv_blocks + n_lam) {
+    // dV and dK of the parts, added in their order: eight elements a thread
+    const size_t rows = static_cast<size_t>(B) * Hkv * Lk;
+    const size_t i = (static_cast<size_t>(blockIdx.x) - conv_blocks - n_lam) * 256 + threadIdx.x;
+    if (i >= rows * (DH / 4)) return;
+    const size_t row = i / (DH / 4);
+    const int m = static_cast<int>(i / (DH / 8)) & 1, c8 = static_cast<int>(i % (DH / 8));
+    float a[8] = {};
+    for (int k = 0; k < n_split; ++k) {
+      const float4* src = reinterpret_cast<const float4*>(
+          kv_part + ((k * rows + row) * 2 + m) * DH + 8 * c8);
+      const float4 u = src[0], v = src[1];
+      a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
+      a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
+    }
+    const float f = m == 0 ? 1.f : scale;
+    uint4 o;
+    o.x = sm100::pack_bf16x2(a[0] * f, a[1] * f);
+    o.y = sm100::pack_bf16x2(a[2] * f, a[3] * f);
+    o.z = sm100::pack_bf16x2(a[4] * f, a[5] * f);
+    o.w = sm100::pack_bf16x2(a[6] * f, a[7] * f);
+    reinterpret_cast<uint4*>((m == 0 ? dV : dK) + row * DH)[c8] = o;
+    return;
+  }
   if (blockIdx.x < conv_blocks) {
     const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const size_t total = static_cast<size_t>(BH) * Lq * (DH / 8);
@@ -240,18 +284,19 @@ __global__ void __launch_bounds__(256)
   }
   const int w = static_cast<int>(blockIdx.x - conv_blocks);
   const int G = Hq / Hkv;
-  // partials [B][Hkv][n_kv][G][NSMX], read in vectors of four; n_lam == 1 adds all of them
+  // partials [B][Hkv][n_kv][n_split][G][NSMX], read in vectors of four; n_lam == 1 adds all
   constexpr int V4 = NSMX / 4;
   const float4* part4 = reinterpret_cast<const float4*>(lam_part);
-  const long long n = static_cast<long long>(B) * n_kv * V4 * (n_lam == 1 ? Hq : 1);
+  const long long per_head = static_cast<long long>(n_kv) * n_split;
+  const long long n = B * per_head * V4 * (n_lam == 1 ? Hq : 1);
   double acc = 0.;
 #pragma unroll 4
   for (long long e = threadIdx.x; e < n; e += 256) {
     long long at = e;
     if (n_lam != 1) {
-      const long long bn = e / V4;  // batch and key tile
-      const long long item = ((bn / n_kv) * Hkv + w / G) * n_kv + bn % n_kv;
-      at = (item * G + w % G) * V4 + e % V4;
+      const long long bn = e / V4;  // batch, key tile and part
+      const long long part_at = ((bn / per_head) * Hkv + w / G) * per_head + bn % per_head;
+      at = (part_at * G + w % G) * V4 + e % V4;
     }
     const float4 v = part4[at];
     acc += static_cast<double>(v.x) + v.y + v.z + v.w;
@@ -384,7 +429,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         *reinterpret_cast<volatile int*>(&item_ring[ik % NI]) = w;
         sm100::mbar_arrive(&item_full[ik % NI]);
         if (w < 0) break;
-        const Item it = get_item(p, w, nullptr);
+        const Part pt = get_part(p, w, nullptr);
+        const Item& it = pt.it;
         if (!(ok = wait(kv_empty, (ik & 1) ^ 1, 43))) break;
         sm100::mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
         ++kv_issued;
@@ -394,7 +440,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           sm100::tma_load_3d(&tmV, kv_full, smem + C::OFF_V + c * PANEL, c * 64, it.n * BN, kvh);
         }
         const int nq = it.T > 0 ? it.T / p.G : 0;
-        for (int t = 0; t < it.T && ok; ++t, ++tq) {
+        for (int t = pt.t0; t < pt.t0 + pt.T && ok; ++t, ++tq) {
           int g, i;
           tile_of(it, t, nq, g, i);
           for (int h = 0; h < 2; ++h) {
@@ -426,9 +472,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       int w;
       if (!(ok = next_item(ik, w)) || w < 0) break;
       if (sm100::lane_id() == 0) {
-        const Item it = get_item(p, w, nullptr);
+        const Part pt = get_part(p, w, nullptr);
+        const Item& it = pt.it;
         const int nq = it.T > 0 ? it.T / p.G : 0;
-        for (int t = 0; t < it.T && ok; ++t, ++tq) {
+        for (int t = pt.t0; t < pt.t0 + pt.T && ok; ++t, ++tq) {
           int g, i;
           tile_of(it, t, nq, g, i);
           const int qh = it.b * p.Hq + it.hkv * p.G + g;
@@ -548,10 +595,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (; ok; ++ik) {
       int w;
       if (!(ok = next_item(ik, w)) || w < 0) break;
-      const Item it = get_item(p, w, nullptr);
+      const Part pt = get_part(p, w, nullptr);
+      const Item& it = pt.it;
+      const int T = pt.T;
       if (!(ok = wait(kv_full, ik & 1, 48))) break;
       sm100::tc_fence_after();
-      if (it.T == 0) {
+      if (T == 0) {
         if (!(ok = wait(dkv_empty, (ik & 1) ^ 1, 49))) break;
         commit(dkv_full);
         commit(kv_empty);
@@ -602,7 +651,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         return true;
       };
       auto next_s = [&](int t, int h) -> bool {
-        if (t + 1 >= it.T) return true;
+        if (t + 1 >= T) return true;
         return wait(s2_read(h), (tq + t) & 1, 55) && first_s(tq + t + 1, h);
       };
       // Issue order: half 1 runs half a tile behind half 0, so that one half's softmax warps
@@ -610,16 +659,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       //   dV_0 dQ_0(t-1) S2_0(t) dK_0(t-1) | S1_1(t) | dP_0(t) |
       //   dV_1 dQ_1(t-1) S2_1(t) dK_1(t-1) | S1_0(t+1) | dP_1(t)
       if (!(ok = first_s(tq, 0))) break;
-      for (int t = 0; t < it.T && ok; ++t)
+      for (int t = 0; t < T && ok; ++t)
         ok = (t == 0 || dv_dq(t - 1, 0)) && second_s(t, 0) &&
              (t == 0 ? first_s(tq, 1) : next_s(t - 1, 1)) && first_dp(t, 0) &&
              (t == 0 || dv_dq(t - 1, 1)) && second_s(t, 1) && next_s(t, 0) && first_dp(t, 1);
       for (int h = 0; h < 2 && ok; ++h) {
-        if (!(ok = dv_dq(it.T - 1, h))) break;
-        both_dk(it.T - 1, h);
+        if (!(ok = dv_dq(T - 1, h))) break;
+        both_dk(T - 1, h);
       }
       if (!ok) break;
-      tq += it.T;
+      tq += T;
       commit(dkv_full);
       commit(kv_empty);
     }
@@ -664,7 +713,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       int w;
       if (!(ok = next_item(ik, w)) || w < 0) break;
       bool bad = false;
-      const Item it = get_item(p, w, &bad);
+      const Part pt = get_part(p, w, &bad);
+      const Item& it = pt.it;
       if (bad && threadIdx.x == 0) atomicOr(p.status, 1);
       const int kvh = it.b * p.Hkv + it.hkv;
       const int key = it.n * BN + kl_;
@@ -672,10 +722,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // (causal), for every c or for none
       const int cmin0 = key >= it.kv_len ? INT_MAX : p.causal ? key - off - 32 * cq : INT_MIN / 2;
       const int cstep = p.causal ? BMQ : 0;
-      const int i_end = it.i_lo + (it.T > 0 ? it.T / p.G : 0);
+      // query head g of the group and query tile i, from the part's first on
+      const int nq = it.T > 0 ? it.T / p.G : 1, i_end = it.i_lo + nq;
+      int g = pt.t0 / nq, i = it.i_lo + pt.t0 % nq;
+      float* lam_part =
+          p.lam_part + ((static_cast<size_t>(kvh) * p.n_kv + it.n) * p.n_split + pt.part) * p.G * NSMX + warp;
+      if (lane == 0)  // heads that this part does not visit
+        for (int e = 0; e < p.G; ++e)
+          if (pt.T == 0 || e < g || e > (pt.t0 + pt.T - 1) / nq) lam_part[e * NSMX] = 0.f;
+      const float* lam = p.lam + (p.n_lam == 1 ? 0 : it.hkv * p.G);
+      const int lam_step = p.n_lam == 1 ? 0 : 1;
+      float nl = pt.T > 0 ? -__ldg(lam + g * lam_step) : 0.f;
+      float2 lam_acc = make_float2(0.f, 0.f);
       // where the next dQ goes
       float* acc = p.dq_acc + (DH == 128 ? 32 * qd + lane : 16 * qd + (lane & 15)) +
-                   (static_cast<size_t>(it.b * p.Hq + it.hkv * p.G) * p.Lqp + it.i_lo * BMQ + 32 * cq) * DH;
+                   (static_cast<size_t>(it.b * p.Hq + it.hkv * p.G + g) * p.Lqp + i * BMQ + 32 * cq) * DH;
       // adds this warp's 32 rows of a tile's dQ^T (lanes = head dimension) into the accumulator
       auto drain_dq = [&](uint32_t tile) -> bool {
         if (!wait_at(DQ_FULL, tile, 65)) return false;
@@ -691,107 +752,109 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         acc += BMQ * DH;
         return true;
       };
-      for (int g = 0; g < p.G && ok; ++g) {
-        float2 lam_acc = make_float2(0.f, 0.f);
-        const float nl = -__ldg(p.lam + (p.n_lam == 1 ? 0 : it.hkv * p.G + g));
-        for (int i = it.i_lo; i < i_end; ++i, ++cur) {
-          const int cmin = cmin0 - i * cstep;
-          const bool all_vis = __all_sync(0xffffffffu, cmin <= 0);
-          const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nlam = make_float2(nl, nl);
-          // ---- P_1, kept in bf16
-          if (!(ok = wait_at(S1_FULL, cur, 59))) break;
-          sm100::tc_fence_after();
-          uint32_t p1[16];
-          {
-            uint32_t s[32];
-            sm100::tmem_ld32(s_addr, s);
-            sm100::tmem_ld_wait();
-            arrive_at(S1_READ);
-            if (!all_vis) {
+      for (int t = 0; t < pt.T; ++t, ++cur) {
+        const int cmin = cmin0 - i * cstep;
+        const bool all_vis = __all_sync(0xffffffffu, cmin <= 0);
+        const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nlam = make_float2(nl, nl);
+        // ---- P_1, kept in bf16
+        if (!(ok = wait_at(S1_FULL, cur, 59))) break;
+        sm100::tc_fence_after();
+        uint32_t p1[16];
+        {
+          uint32_t s[32];
+          sm100::tmem_ld32(s_addr, s);
+          sm100::tmem_ld_wait();
+          arrive_at(S1_READ);
+          if (!all_vis) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (c < cmin) s[c] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < 32; ++c)
+              if (c < cmin) s[c] = __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int c4 = 0; c4 < 8; ++c4) {
+            const float4 nlse = l1v[c4];
+            const float2 n2[2] = {make_float2(nlse.x, nlse.y), make_float2(nlse.z, nlse.w)};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int cp = 2 * c4 + e;
+              const float2 x = __ffma2_rn(f2(s[2 * cp], s[2 * cp + 1]), sl2, n2[e]);
+              p1[cp] = sm100::pack_bf16x2(sm100::ex2(x.x), sm100::ex2(x.y));
             }
+          }
+        }
+        // ---- the previous tile's dQ
+        if (t > 0 && !(ok = drain_dq(cur - 1))) break;
+        if (t > 0 && i == it.i_lo)  // that was the last tile of the head before
+          acc += static_cast<size_t>(p.Lqp - nq * BMQ) * DH;
+        // ---- sixteen columns at a time: P_2, W = P_1 - lam P_2 (over the dP it goes with),
+        // dS_1 = P_1 (dP - D_1), dS_2 = P_2 (-lam dP + lam D_2), row-contiguous per key,
+        // 16-byte chunk q of line kl_ at q ^ (kl_ & 7)
+        if (!(ok = wait_at(DP_FULL, cur, 62))) break;
+        sm100::tc_fence_after();
 #pragma unroll
-            for (int c4 = 0; c4 < 8; ++c4) {
-              const float4 nlse = l1v[c4];
-              const float2 n2[2] = {make_float2(nlse.x, nlse.y), make_float2(nlse.z, nlse.w)};
+        for (int k = 0; k < 2; ++k) {
+          uint32_t s[16], dp[16], wv[16];  // wv: W, then dS_1, eight words each
+          sm100::tmem_ld16(s_addr + 16 * k, s);
+          sm100::tmem_ld16(dp_addr + 16 * k, dp);
+          sm100::tmem_ld_wait();
+          if (k == 1) arrive_at(S2_READ);
+          if (!all_vis) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (16 * k + c < cmin) s[c] = __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {  // eight columns: one 16-byte chunk of each map
+            uint32_t w1[4], w2[4];
+#pragma unroll
+            for (int c4 = 0; c4 < 2; ++c4) {
+              const int cc = 4 * k + 2 * q + c4;  // columns 4 cc ... of the thread's 32
+              const float4 nl4 = l2v[cc], n1 = d1v[cc], n2 = d2v[cc];
+              const float2 nlse[2] = {make_float2(nl4.x, nl4.y), make_float2(nl4.z, nl4.w)};
+              const float2 nd1[2] = {make_float2(n1.x, n1.y), make_float2(n1.z, n1.w)};
+              const float2 ld2[2] = {make_float2(n2.x, n2.y), make_float2(n2.z, n2.w)};
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int cp = 2 * c4 + e;
-                const float2 x = __ffma2_rn(f2(s[2 * cp], s[2 * cp + 1]), sl2, n2[e]);
-                p1[cp] = sm100::pack_bf16x2(sm100::ex2(x.x), sm100::ex2(x.y));
+                const int j = 8 * q + 4 * c4 + 2 * e;  // of the sixteen columns
+                const uint32_t u = p1[2 * cc + e];
+                const float2 pa = f2(u << 16, u & 0xFFFF0000u), gp = f2(dp[j], dp[j + 1]);
+                const float2 x = __ffma2_rn(f2(s[j], s[j + 1]), sl2, nlse[e]);
+                const float2 pb = make_float2(sm100::ex2(x.x), sm100::ex2(x.y));
+                const float2 wf = __ffma2_rn(pb, nlam, pa);
+                const float2 a = __fmul2_rn(pa, __fadd2_rn(gp, nd1[e]));
+                const float2 b = __fmul2_rn(pb, __ffma2_rn(gp, nlam, ld2[e]));
+                lam_acc = __ffma2_rn(pb, gp, lam_acc);
+                wv[4 * q + 2 * c4 + e] = sm100::pack_bf16x2(wf.x, wf.y);
+                w1[2 * c4 + e] = sm100::pack_bf16x2(a.x, a.y);
+                w2[2 * c4 + e] = sm100::pack_bf16x2(b.x, b.y);
               }
             }
+            const uint32_t at = line + (((4 * (cq & 1) + 2 * k + q) ^ (kl_ & 7)) << 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) wv[8 + 4 * q + e] = w1[e];
+            st_shared_v4(at, w1);
+            st_shared_v4(at + 2 * PANEL, w2);
           }
-          // ---- the previous tile's dQ
-          if ((i > it.i_lo || g > 0) && !(ok = drain_dq(cur - 1))) break;
-          if (i == it.i_lo && g > 0)  // that was the last tile of the head before
-            acc += static_cast<size_t>(p.Lqp - (i_end - it.i_lo) * BMQ) * DH;
-          // ---- sixteen columns at a time: P_2, W = P_1 - lam P_2 (over the dP it goes with),
-          // dS_1 = P_1 (dP - D_1), dS_2 = P_2 (-lam dP + lam D_2), row-contiguous per key,
-          // 16-byte chunk q of line kl_ at q ^ (kl_ & 7)
-          if (!(ok = wait_at(DP_FULL, cur, 62))) break;
-          sm100::tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t s[16], dp[16], wv[16];  // wv: W, then dS_1, eight words each
-            sm100::tmem_ld16(s_addr + 16 * k, s);
-            sm100::tmem_ld16(dp_addr + 16 * k, dp);
-            sm100::tmem_ld_wait();
-            if (k == 1) arrive_at(S2_READ);
-            if (!all_vis) {
-#pragma unroll
-              for (int c = 0; c < 16; ++c)
-                if (16 * k + c < cmin) s[c] = __float_as_uint(-INFINITY);
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {  // eight columns: one 16-byte chunk of each map
-              uint32_t w1[4], w2[4];
-#pragma unroll
-              for (int c4 = 0; c4 < 2; ++c4) {
-                const int cc = 4 * k + 2 * q + c4;  // columns 4 cc ... of the thread's 32
-                const float4 nl4 = l2v[cc], n1 = d1v[cc], n2 = d2v[cc];
-                const float2 nlse[2] = {make_float2(nl4.x, nl4.y), make_float2(nl4.z, nl4.w)};
-                const float2 nd1[2] = {make_float2(n1.x, n1.y), make_float2(n1.z, n1.w)};
-                const float2 ld2[2] = {make_float2(n2.x, n2.y), make_float2(n2.z, n2.w)};
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int j = 8 * q + 4 * c4 + 2 * e;  // of the sixteen columns
-                  const uint32_t u = p1[2 * cc + e];
-                  const float2 pa = f2(u << 16, u & 0xFFFF0000u), gp = f2(dp[j], dp[j + 1]);
-                  const float2 x = __ffma2_rn(f2(s[j], s[j + 1]), sl2, nlse[e]);
-                  const float2 pb = make_float2(sm100::ex2(x.x), sm100::ex2(x.y));
-                  const float2 wf = __ffma2_rn(pb, nlam, pa);
-                  const float2 a = __fmul2_rn(pa, __fadd2_rn(gp, nd1[e]));
-                  const float2 b = __fmul2_rn(pb, __ffma2_rn(gp, nlam, ld2[e]));
-                  lam_acc = __ffma2_rn(pb, gp, lam_acc);
-                  wv[4 * q + 2 * c4 + e] = sm100::pack_bf16x2(wf.x, wf.y);
-                  w1[2 * c4 + e] = sm100::pack_bf16x2(a.x, a.y);
-                  w2[2 * c4 + e] = sm100::pack_bf16x2(b.x, b.y);
-                }
-              }
-              const uint32_t at = line + (((4 * (cq & 1) + 2 * k + q) ^ (kl_ & 7)) << 4);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) wv[8 + 4 * q + e] = w1[e];
-              st_shared_v4(at, w1);
-              st_shared_v4(at + 2 * PANEL, w2);
-            }
-            sm100::tmem_st16(dp_addr + 16 * k, wv);
-          }
-          sm100::tmem_st_wait();
-          sm100::fence_proxy_async_smem();
-          arrive_at(DS_FULL);
+          sm100::tmem_st16(dp_addr + 16 * k, wv);
         }
-        if (!ok) break;
-        float x = lam_acc.x + lam_acc.y;
+        sm100::tmem_st_wait();
+        sm100::fence_proxy_async_smem();
+        arrive_at(DS_FULL);
+        if (++i == i_end || t + 1 == pt.T) {  // the part's last tile of the head
+          float x = lam_acc.x + lam_acc.y;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0)
-          p.lam_part[((static_cast<size_t>(kvh) * p.n_kv + it.n) * p.G + g) * NSMX + warp] = x;
+          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+          if (lane == 0) lam_part[g * NSMX] = x;
+          lam_acc = make_float2(0.f, 0.f);
+          if (i == i_end && t + 1 < pt.T) {
+            i = it.i_lo;
+            ++g;
+            nl = -__ldg(lam + g * lam_step);
+          }
+        }
       }
       if (!ok) break;
-      if (it.T > 0 && !(ok = drain_dq(cur - 1))) break;
+      if (pt.T > 0 && !(ok = drain_dq(cur - 1))) break;
       // ---------------- epilogue: dV, dK (x scale) of this key row, a quarter of the columns
       if (!(ok = wait(dkv_full, ik & 1, 64))) break;
       sm100::tc_fence_after();
@@ -814,10 +877,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           sm100::tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            o[e] = it.T > 0 ? sm100::pack_bf16x2(__uint_as_float(v[2 * e]) * f,
+            o[e] = pt.T > 0 ? sm100::pack_bf16x2(__uint_as_float(v[2 * e]) * f,
                                                  __uint_as_float(v[2 * e + 1]) * f)
                             : 0u;
-          if (live) {
+          if (p.n_split > 1) {  // the parts' sums are added, scaled and rounded at the end
+            if (live) {
+              if (pt.T == 0)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = 0u;
+              float* part = p.kv_part +
+                            ((static_cast<size_t>(pt.part) * p.B * p.Hkv * p.Lk + orow) * 2 + m) * DH +
+                            DQ * cq + c;
+              st_global_v8(part, v);
+              st_global_v8(part + 8, v + 8);
+            }
+          } else if (live) {
             if (wide) {
               st_global_v8(dst + c, o);
             } else {
@@ -860,26 +934,63 @@ struct Args : attn_bwd_impl::Args {
   __nv_bfloat16* dlam;
 };
 
-// fp32 accumulator, statistics and dlam partials
+// Parts that the items' query tiles are shared out to.  An item -- 128 keys of one key/value
+// head -- walks the query tiles of every head of the group, so a few key/value heads, or
+// the causal mask's unequal items, leave SMs idle behind the longest one.  In units of a
+// tile, a part costs about one more (its K, V, first products and sums); the makespan
+// is the larger of the mean load and the longest part, and the least estimate wins.
+// Measured on B200: B3 Hq16 Hkv4 L1999 d64 (192 items of up to 64 tiles) 1 part 207 us,
+// 2 parts see the table of the backward in the design notes.
+inline int n_split(int B, int Hq, int Hkv, int Lq, int Lk, bool causal) {
+  constexpr double SMS = 148.;
+  const double items = static_cast<double>(B) * Hkv * ((Lk + BN - 1) / BN);
+  const double longest = static_cast<double>(Hq / Hkv) * ((Lq + BMQ - 1) / BMQ);
+  if (items <= 0. || longest <= 0.) return 1;
+  const double mean = items * longest * (causal && Lq > BMQ ? 0.5 : 1.0) / SMS;
+  int best = 1;
+  double least = 0.;
+  for (int s = 1; s <= 64 && s <= longest; ++s) {
+    const double part = longest / s + 1.;
+    double load = mean + items * s / SMS;
+    if (!causal) load = ceil(items * s / SMS) * part;  // equal parts run in waves
+    const double est = part > load ? part : load;
+    if (s == 1 || est < 0.95 * least) {
+      best = s;
+      least = est;
+    }
+  }
+  return best;
+}
+
+// fp32 accumulator, statistics, dlam partials and the parts' dV and dK
 struct Scratch {
-  size_t acc, stats, part, total;
+  size_t acc, stats, lam, kv, total;
 };
-inline Scratch scratch(int B, int Hq, int Lq, int Lk, int d) {
+inline Scratch scratch(int B, int Hq, int Hkv, int Lq, int Lk, int d, int split) {
   const size_t rows = static_cast<size_t>(B) * Hq * attn_bwd_impl::lq_pad(Lq);
   const size_t n_kv = (static_cast<size_t>(Lk) + BN - 1) / BN;
   Scratch s;
   s.acc = 0;
   s.stats = rows * d * 4;
-  s.part = s.stats + rows * 16;
-  s.total = (s.part + static_cast<size_t>(B) * Hq * n_kv * NSMX * 4 + 255) & ~static_cast<size_t>(255);
+  s.lam = s.stats + rows * 16;
+  s.kv = s.lam + static_cast<size_t>(B) * Hq * n_kv * split * NSMX * 4;
+  s.total = s.kv;
+  if (split > 1) s.total += static_cast<size_t>(split) * B * Hkv * Lk * d * 8;
+  s.total = (s.total + 255) & ~static_cast<size_t>(255);
   return s;
+}
+inline size_t scratch_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int d) {  // for either mask
+  const size_t a = scratch(B, Hq, Hkv, Lq, Lk, d, n_split(B, Hq, Hkv, Lq, Lk, false)).total;
+  const size_t c = scratch(B, Hq, Hkv, Lq, Lk, d, n_split(B, Hq, Hkv, Lq, Lk, true)).total;
+  return a > c ? a : c;
 }
 
 template <int DH>
 attn_status_t launch_d(const Args& a, cudaStream_t s) {
   using C = Cfg<DH>;
   Params p{};
-  const Scratch sc = scratch(a.B, a.Hq, a.Lq, a.Lk, DH);
+  p.n_split = n_split(a.B, a.Hq, a.Hkv, a.Lq, a.Lk, a.causal != 0);
+  const Scratch sc = scratch(a.B, a.Hq, a.Hkv, a.Lq, a.Lk, DH, p.n_split);
   p.B = a.B;
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
@@ -897,11 +1008,12 @@ attn_status_t launch_d(const Args& a, cudaStream_t s) {
   p.dV = a.dV;
   p.n_kv = (a.Lk + BN - 1) / BN;
   p.n_qt = p.Lqp / BMQ;
-  p.n_items = a.B * a.Hkv * p.n_kv;
+  p.n_items = a.B * a.Hkv * p.n_kv * p.n_split;
   p.dq_acc = reinterpret_cast<float*>(a.scratch + sc.acc);
   float* stats = reinterpret_cast<float*>(a.scratch + sc.stats);
   p.stats = stats;
-  p.lam_part = reinterpret_cast<float*>(a.scratch + sc.part);
+  p.lam_part = reinterpret_cast<float*>(a.scratch + sc.lam);
+  p.kv_part = reinterpret_cast<float*>(a.scratch + sc.kv);
   p.lam = a.lam;
   p.n_lam = a.n_lam;
   const long long BH = static_cast<long long>(a.B) * a.Hq;
@@ -936,11 +1048,13 @@ attn_status_t launch_d(const Args& a, cudaStream_t s) {
       return ATTN_ERR_CUDA;
   }
   const long long conv = (BH * a.Lq * (DH / 8) + 255) / 256;
+  const long long kv =
+      p.n_split > 1 ? (static_cast<long long>(a.B) * a.Hkv * a.Lk * (DH / 4) + 255) / 256 : 0;
   return attn_host::report(
-             attn_host::launch_overlapped(finish_kernel<DH>, dim3(static_cast<unsigned>(conv + a.n_lam)),
-                                          dim3(256), 0, s, p.dq_acc, a.dQ, BH, a.Lq, p.Lqp, a.scale,
-                                          conv, p.lam_part, a.dlam, a.B, a.Hq, a.Hkv, p.n_kv,
-                                          a.n_lam),
+             attn_host::launch_overlapped(
+                 finish_kernel<DH>, dim3(static_cast<unsigned>(conv + a.n_lam + kv)), dim3(256), 0,
+                 s, p.dq_acc, a.dQ, BH, a.Lq, p.Lqp, a.scale, conv, p.lam_part, a.dlam, a.B, a.Hq,
+                 a.Hkv, a.Lk, a.n_lam, p.n_split, p.kv_part, a.dK, a.dV),
              "diff finish_kernel") == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_CUDA;

@@ -222,7 +222,8 @@ attn_status_t attn_fwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const at
  *   bf16, finite.  dQ [B,Hq,Lq,d], dK, dV [B,Hkv,Lk,d] and dlam [n_lam] are
  *   written, all bf16, with dK = dV = 0 at and past k_lens[b].  Masks, limits and
  *   errors as attn_fwd_diff.  The workspace holds the fp32 dQ accumulator, four
- *   fp32 statistics per query row and the partial sums of dlam.  dQ's sums are
+ *   fp32 statistics per query row, the partial sums of dlam and, where there are
+ *   few key/value heads and keys, fp32 partial sums of dV and dK.  dQ's sums are
  *   formed in no fixed order (its last bit may differ from run to run); dK, dV and
  *   dlam are the same each time.
  */

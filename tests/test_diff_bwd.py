@@ -72,6 +72,10 @@ CASES = [
     (2, 2, 1, 300, 300, 128, True, [0, 300]),      # a sequence without a key
     (1, 3, 3, 17, 600, 128, False, [513]),
     (3, 2, 2, 520, 520, 128, True, [384, 128, 520]),
+    # (those above have few enough items to be split; these are not)
+    (8, 16, 16, 300, 300, 64, True, [300, 1, 128, 129, 255, 256, 257, 290]),
+    (5, 20, 10, 260, 390, 128, False, None),
+    (1, 16, 1, 700, 700, 128, True, None),         # one key/value head: parts of several heads
 ]
 
 
@@ -276,14 +280,16 @@ def test_bwd_rejects_on_host():
 
 
 def test_bwd_workspace_is_a_closed_form():
-    """fp32 dQ accumulator and four statistics per query row (padded to 128 per head), and 16
-    partial sums of dlam per (sequence, head, 128-key tile)."""
+    """fp32 dQ accumulator and four statistics per query row (padded to 128 per head), 16 partial
+    sums of dlam per (sequence, head, 128-key tile, part), and with several parts each
+    one's fp32 dV and dK."""
     attn = _lib()
 
-    def want(B, Hq, Lq, Lk, d):
+    def want(B, Hq, Hkv, Lq, Lk, d, parts):
         rows = B * Hq * ((max(Lq, 1) + 127) // 128 * 128)
-        n = rows * d * 4 + rows * 16 + B * Hq * ((Lk + 127) // 128) * 64
+        n = rows * d * 4 + rows * 16 + B * Hq * ((Lk + 127) // 128) * parts * 64
+        n += parts * B * Hkv * Lk * d * 8 if parts > 1 else 0
         return 256 + (n + 255) // 256 * 256
 
-    for B, Hq, Hkv, Lq, Lk, d in ((2, 16, 16, 8192, 8192, 128), (1, 6, 2, 100, 300, 64)):
-        assert attn.attn_bwd_diff_workspace_size(B, Hq, Hkv, Lq, Lk, d) == want(B, Hq, Lq, Lk, d)
+    for a, parts in (((2, 16, 16, 8192, 8192, 128), 1), ((1, 6, 2, 100, 300, 64), 3)):
+        assert attn.attn_bwd_diff_workspace_size(*a) == want(*a, parts)
