@@ -140,21 +140,13 @@ __device__ __forceinline__ Part get_part(const Params& p, int w, bool* bad) {
   return q;
 }
 
-// sm100::mbar_wait with the slow path out of line and a longer suspension per try: the
-// waiting warps' polls otherwise take issue slots and shared-memory accesses from the others.
+// sm100::mbar_wait by shared address, its slow path out of line: inlined at every wait it cost
+// registers that the softmax warps need (1907 against 1957 us).
 __device__ __noinline__ bool mbar_wait_slow(uint32_t a, uint32_t parity, volatile int* abort,
                                             int* status, int site) {
   const long long t0 = clock64();
   for (uint32_t it = 0; it < 0x40000000u; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(a), "r"(parity), "r"(2000u)  // ns
-        : "memory");
-    if (ok) return true;
+    if (sm100::mbar_try_wait(a, parity)) return true;
     if (*abort) return false;
     if (clock64() - t0 > ATTN_WAIT_CYCLES) break;
   }
@@ -732,8 +724,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (pt.T == 0 || e < g || e > (pt.t0 + pt.T - 1) / nq) lam_part[e * NSMX] = 0.f;
       const float* lam = p.lam + (p.n_lam == 1 ? 0 : it.hkv * p.G);
       const int lam_step = p.n_lam == 1 ? 0 : 1;
-      float nl = pt.T > 0 ? -__ldg(lam + g * lam_step) : 0.f;
-      float2 lam_acc = make_float2(0.f, 0.f);
       // where the next dQ goes
       float* acc = p.dq_acc + (DH == 128 ? 32 * qd + lane : 16 * qd + (lane & 15)) +
                    (static_cast<size_t>(it.b * p.Hq + it.hkv * p.G + g) * p.Lqp + i * BMQ + 32 * cq) * DH;
@@ -752,106 +742,107 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         acc += BMQ * DH;
         return true;
       };
-      for (int t = 0; t < pt.T; ++t, ++cur) {
-        const int cmin = cmin0 - i * cstep;
-        const bool all_vis = __all_sync(0xffffffffu, cmin <= 0);
-        const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nlam = make_float2(nl, nl);
-        // ---- P_1, kept in bf16
-        if (!(ok = wait_at(S1_FULL, cur, 59))) break;
-        sm100::tc_fence_after();
-        uint32_t p1[16];
-        {
-          uint32_t s[32];
-          sm100::tmem_ld32(s_addr, s);
-          sm100::tmem_ld_wait();
-          arrive_at(S1_READ);
-          if (!all_vis) {
+      const uint32_t cur0 = cur;
+      for (int left = pt.T; left > 0 && ok; ++g) {  // a head's tiles of the part
+        const int i_stop = min(i_end, i + left);
+        left -= i_stop - i;
+        const float nl = -__ldg(lam + g * lam_step);
+        float2 lam_acc = make_float2(0.f, 0.f);
+        for (; i < i_stop; ++i, ++cur) {
+          const int cmin = cmin0 - i * cstep;
+          const bool all_vis = __all_sync(0xffffffffu, cmin <= 0);
+          const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nlam = make_float2(nl, nl);
+          // ---- P_1, kept in bf16
+          if (!(ok = wait_at(S1_FULL, cur, 59))) break;
+          sm100::tc_fence_after();
+          uint32_t p1[16];
+          {
+            uint32_t s[32];
+            sm100::tmem_ld32(s_addr, s);
+            sm100::tmem_ld_wait();
+            arrive_at(S1_READ);
+            if (!all_vis) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (c < cmin) s[c] = __float_as_uint(-INFINITY);
-          }
-#pragma unroll
-          for (int c4 = 0; c4 < 8; ++c4) {
-            const float4 nlse = l1v[c4];
-            const float2 n2[2] = {make_float2(nlse.x, nlse.y), make_float2(nlse.z, nlse.w)};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int cp = 2 * c4 + e;
-              const float2 x = __ffma2_rn(f2(s[2 * cp], s[2 * cp + 1]), sl2, n2[e]);
-              p1[cp] = sm100::pack_bf16x2(sm100::ex2(x.x), sm100::ex2(x.y));
+              for (int c = 0; c < 32; ++c)
+                if (c < cmin) s[c] = __float_as_uint(-INFINITY);
             }
-          }
-        }
-        // ---- the previous tile's dQ
-        if (t > 0 && !(ok = drain_dq(cur - 1))) break;
-        if (t > 0 && i == it.i_lo)  // that was the last tile of the head before
-          acc += static_cast<size_t>(p.Lqp - nq * BMQ) * DH;
-        // ---- sixteen columns at a time: P_2, W = P_1 - lam P_2 (over the dP it goes with),
-        // dS_1 = P_1 (dP - D_1), dS_2 = P_2 (-lam dP + lam D_2), row-contiguous per key,
-        // 16-byte chunk q of line kl_ at q ^ (kl_ & 7)
-        if (!(ok = wait_at(DP_FULL, cur, 62))) break;
-        sm100::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t s[16], dp[16], wv[16];  // wv: W, then dS_1, eight words each
-          sm100::tmem_ld16(s_addr + 16 * k, s);
-          sm100::tmem_ld16(dp_addr + 16 * k, dp);
-          sm100::tmem_ld_wait();
-          if (k == 1) arrive_at(S2_READ);
-          if (!all_vis) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (16 * k + c < cmin) s[c] = __float_as_uint(-INFINITY);
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {  // eight columns: one 16-byte chunk of each map
-            uint32_t w1[4], w2[4];
-#pragma unroll
-            for (int c4 = 0; c4 < 2; ++c4) {
-              const int cc = 4 * k + 2 * q + c4;  // columns 4 cc ... of the thread's 32
-              const float4 nl4 = l2v[cc], n1 = d1v[cc], n2 = d2v[cc];
-              const float2 nlse[2] = {make_float2(nl4.x, nl4.y), make_float2(nl4.z, nl4.w)};
-              const float2 nd1[2] = {make_float2(n1.x, n1.y), make_float2(n1.z, n1.w)};
-              const float2 ld2[2] = {make_float2(n2.x, n2.y), make_float2(n2.z, n2.w)};
+            for (int c4 = 0; c4 < 8; ++c4) {
+              const float4 nlse = l1v[c4];
+              const float2 n2[2] = {make_float2(nlse.x, nlse.y), make_float2(nlse.z, nlse.w)};
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int j = 8 * q + 4 * c4 + 2 * e;  // of the sixteen columns
-                const uint32_t u = p1[2 * cc + e];
-                const float2 pa = f2(u << 16, u & 0xFFFF0000u), gp = f2(dp[j], dp[j + 1]);
-                const float2 x = __ffma2_rn(f2(s[j], s[j + 1]), sl2, nlse[e]);
-                const float2 pb = make_float2(sm100::ex2(x.x), sm100::ex2(x.y));
-                const float2 wf = __ffma2_rn(pb, nlam, pa);
-                const float2 a = __fmul2_rn(pa, __fadd2_rn(gp, nd1[e]));
-                const float2 b = __fmul2_rn(pb, __ffma2_rn(gp, nlam, ld2[e]));
-                lam_acc = __ffma2_rn(pb, gp, lam_acc);
-                wv[4 * q + 2 * c4 + e] = sm100::pack_bf16x2(wf.x, wf.y);
-                w1[2 * c4 + e] = sm100::pack_bf16x2(a.x, a.y);
-                w2[2 * c4 + e] = sm100::pack_bf16x2(b.x, b.y);
+                const int cp = 2 * c4 + e;
+                const float2 x = __ffma2_rn(f2(s[2 * cp], s[2 * cp + 1]), sl2, n2[e]);
+                p1[cp] = sm100::pack_bf16x2(sm100::ex2(x.x), sm100::ex2(x.y));
               }
             }
-            const uint32_t at = line + (((4 * (cq & 1) + 2 * k + q) ^ (kl_ & 7)) << 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) wv[8 + 4 * q + e] = w1[e];
-            st_shared_v4(at, w1);
-            st_shared_v4(at + 2 * PANEL, w2);
           }
-          sm100::tmem_st16(dp_addr + 16 * k, wv);
-        }
-        sm100::tmem_st_wait();
-        sm100::fence_proxy_async_smem();
-        arrive_at(DS_FULL);
-        if (++i == i_end || t + 1 == pt.T) {  // the part's last tile of the head
-          float x = lam_acc.x + lam_acc.y;
+          // ---- the previous tile's dQ
+          if (cur != cur0 && !(ok = drain_dq(cur - 1))) break;
+          if (cur != cur0 && i == it.i_lo)  // that was the last tile of the head before
+            acc += static_cast<size_t>(p.Lqp - nq * BMQ) * DH;
+          // ---- sixteen columns at a time: P_2, W = P_1 - lam P_2 (over the dP it goes with),
+          // dS_1 = P_1 (dP - D_1), dS_2 = P_2 (-lam dP + lam D_2), row-contiguous per key,
+          // 16-byte chunk q of line kl_ at q ^ (kl_ & 7)
+          if (!(ok = wait_at(DP_FULL, cur, 62))) break;
+          sm100::tc_fence_after();
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (lane == 0) lam_part[g * NSMX] = x;
-          lam_acc = make_float2(0.f, 0.f);
-          if (i == i_end && t + 1 < pt.T) {
-            i = it.i_lo;
-            ++g;
-            nl = -__ldg(lam + g * lam_step);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t s[16], dp[16], wv[16];  // wv: W, then dS_1, eight words each
+            sm100::tmem_ld16(s_addr + 16 * k, s);
+            sm100::tmem_ld16(dp_addr + 16 * k, dp);
+            sm100::tmem_ld_wait();
+            if (k == 1) arrive_at(S2_READ);
+            if (!all_vis) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (16 * k + c < cmin) s[c] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {  // eight columns: one 16-byte chunk of each map
+              uint32_t w1[4], w2[4];
+#pragma unroll
+              for (int c4 = 0; c4 < 2; ++c4) {
+                const int cc = 4 * k + 2 * q + c4;  // columns 4 cc ... of the thread's 32
+                const float4 nl4 = l2v[cc], n1 = d1v[cc], n2 = d2v[cc];
+                const float2 nlse[2] = {make_float2(nl4.x, nl4.y), make_float2(nl4.z, nl4.w)};
+                const float2 nd1[2] = {make_float2(n1.x, n1.y), make_float2(n1.z, n1.w)};
+                const float2 ld2[2] = {make_float2(n2.x, n2.y), make_float2(n2.z, n2.w)};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int j = 8 * q + 4 * c4 + 2 * e;  // of the sixteen columns
+                  const uint32_t u = p1[2 * cc + e];
+                  const float2 pa = f2(u << 16, u & 0xFFFF0000u), gp = f2(dp[j], dp[j + 1]);
+                  const float2 x = __ffma2_rn(f2(s[j], s[j + 1]), sl2, nlse[e]);
+                  const float2 pb = make_float2(sm100::ex2(x.x), sm100::ex2(x.y));
+                  const float2 wf = __ffma2_rn(pb, nlam, pa);
+                  const float2 a = __fmul2_rn(pa, __fadd2_rn(gp, nd1[e]));
+                  const float2 b = __fmul2_rn(pb, __ffma2_rn(gp, nlam, ld2[e]));
+                  lam_acc = __ffma2_rn(pb, gp, lam_acc);
+                  wv[4 * q + 2 * c4 + e] = sm100::pack_bf16x2(wf.x, wf.y);
+                  w1[2 * c4 + e] = sm100::pack_bf16x2(a.x, a.y);
+                  w2[2 * c4 + e] = sm100::pack_bf16x2(b.x, b.y);
+                }
+              }
+              const uint32_t at = line + (((4 * (cq & 1) + 2 * k + q) ^ (kl_ & 7)) << 4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) wv[8 + 4 * q + e] = w1[e];
+              st_shared_v4(at, w1);
+              st_shared_v4(at + 2 * PANEL, w2);
+            }
+            sm100::tmem_st16(dp_addr + 16 * k, wv);
           }
+          sm100::tmem_st_wait();
+          sm100::fence_proxy_async_smem();
+          arrive_at(DS_FULL);
         }
+        if (!ok) break;
+        float x = lam_acc.x + lam_acc.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) lam_part[g * NSMX] = x;
+        i = it.i_lo;
       }
       if (!ok) break;
       if (pt.T > 0 && !(ok = drain_dq(cur - 1))) break;
