@@ -53,8 +53,11 @@
 // from run to run.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include <climits>
 #include <cmath>
+#include <cstring>
 
 #include "bwd_kernel.cuh"
 
@@ -108,8 +111,8 @@ __host__ __device__ constexpr int acc_pos(int c) {
 }
 
 // TMEM columns
-constexpr uint32_t S_COL = 0;     // S_m^T; W^T in the first 16 of each warp's 32 columns
-constexpr uint32_t DP_COL = 128;  // dP^T, then dQ_1^T and dQ_2^T in alternate 16 lanes
+constexpr uint32_t S_COL = 0;     // S_m^T
+constexpr uint32_t DP_COL = 128;  // dP^T; W^T and dS_1^T (8 of every 16 columns each); dQ^T of both maps
 constexpr uint32_t DV_COL = 256;
 constexpr uint32_t DK_COL = 384;  // dK_1, dK_2 (64 each)
 
@@ -118,7 +121,8 @@ constexpr uint32_t DK_COL = 384;  // dK_1, dK_2 (64 each)
 // unit, are short.
 
 struct Params : attn_bwd_impl::Params {
-  const float* stats;  // [B*Hq][n_qt][2 halves][4][64]: -lse2_1, -lse2_2, -D_1, lam D_2
+  // [B*Hq][n_qt][2 halves][4][64]: -lse2_1, -lse2_2 (both plus P_SCALE_LOG2), -D_1, lam D_2
+  const float* stats;
   const float* lam;    // [n_lam]
   int n_lam;
   float* lam_part;  // [B*Hkv][n_kv][n_split][G][NSMX] sums of P_2 dP
@@ -138,6 +142,23 @@ __device__ __forceinline__ Part get_part(const Params& p, int w, bool* bad) {
   q.t0 = static_cast<int>(static_cast<long long>(q.it.T) * q.part / p.n_split);
   q.T = static_cast<int>(static_cast<long long>(q.it.T) * (q.part + 1) / p.n_split) - q.t0;
   return q;
+}
+
+// Every probability is formed 2^14 times too large (in the statistics' exponent), and the
+// outputs' factors take that back.  P_1 waits in 16 bits for dP: as fp16 its rounding is
+// 2^-12 relative instead of bf16's 2^-9, which would be as large as that of dS itself, and the
+// scale keeps that down to probabilities of 4e-9 (one of 1 becomes 16384, of 65504).
+constexpr float P_SCALE_LOG2 = 14.f, P_UNSCALE = 1.f / 16384.f;
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
+  __half2 h;
+  memcpy(&h, &v, 4);
+  return __half22float2(h);
 }
 
 // sm100::mbar_wait by shared address, its slow path out of line: inlined at every wait it cost
@@ -211,7 +232,8 @@ __global__ void __launch_bounds__(256)
     const float l = __ldg(lam + (n_lam == 1 ? 0 : h));
     float v;
     if (lane < 2) {  // -inf where the row sees no key or lies past Lq: P is exactly 0
-      v = r < Lq ? -lse[(static_cast<size_t>(bh) * 2 + lane) * Lq + r] * 1.4426950408889634f
+      v = r < Lq ? P_SCALE_LOG2 - lse[(static_cast<size_t>(bh) * 2 + lane) * Lq + r] *
+                                      1.4426950408889634f
                  : -INFINITY;
       if (v == INFINITY) v = -INFINITY;
     } else {
@@ -247,7 +269,7 @@ __global__ void __launch_bounds__(256)
       a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
       a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
     }
-    const float f = m == 0 ? 1.f : scale;
+    const float f = (m == 0 ? 1.f : scale) * P_UNSCALE;
     uint4 o;
     o.x = sm100::pack_bf16x2(a[0] * f, a[1] * f);
     o.y = sm100::pack_bf16x2(a[2] * f, a[3] * f);
@@ -257,6 +279,7 @@ __global__ void __launch_bounds__(256)
     return;
   }
   if (blockIdx.x < conv_blocks) {
+    scale *= P_UNSCALE;
     const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const size_t total = static_cast<size_t>(BH) * Lq * (DH / 8);
     if (i >= total) return;
@@ -300,7 +323,8 @@ __global__ void __launch_bounds__(256)
     if (threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
     __syncthreads();
   }
-  if (threadIdx.x == 0) dlam[w] = __float2bfloat16_rn(static_cast<float>(-part[0]));
+  if (threadIdx.x == 0)
+    dlam[w] = __float2bfloat16_rn(static_cast<float>(-part[0] * P_UNSCALE));
 }
 
 // ------------------------------------------------------------------ main
@@ -752,7 +776,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           const int cmin = cmin0 - i * cstep;
           const bool all_vis = __all_sync(0xffffffffu, cmin <= 0);
           const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nlam = make_float2(nl, nl);
-          // ---- P_1, kept in bf16
+          // ---- P_1, kept in fp16 (see P_SCALE)
           if (!(ok = wait_at(S1_FULL, cur, 59))) break;
           sm100::tc_fence_after();
           uint32_t p1[16];
@@ -774,7 +798,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               for (int e = 0; e < 2; ++e) {
                 const int cp = 2 * c4 + e;
                 const float2 x = __ffma2_rn(f2(s[2 * cp], s[2 * cp + 1]), sl2, n2[e]);
-                p1[cp] = sm100::pack_bf16x2(sm100::ex2(x.x), sm100::ex2(x.y));
+                p1[cp] = pack_f16x2(sm100::ex2(x.x), sm100::ex2(x.y));
               }
             }
           }
@@ -812,8 +836,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const int j = 8 * q + 4 * c4 + 2 * e;  // of the sixteen columns
-                  const uint32_t u = p1[2 * cc + e];
-                  const float2 pa = f2(u << 16, u & 0xFFFF0000u), gp = f2(dp[j], dp[j + 1]);
+                  const float2 pa = unpack_f16x2(p1[2 * cc + e]), gp = f2(dp[j], dp[j + 1]);
                   const float2 x = __ffma2_rn(f2(s[j], s[j + 1]), sl2, nlse[e]);
                   const float2 pb = make_float2(sm100::ex2(x.x), sm100::ex2(x.y));
                   const float2 wf = __ffma2_rn(pb, nlam, pa);
@@ -857,7 +880,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
       for (int m = 0; m < 2; ++m) {
         __nv_bfloat16* dst = (m == 0 ? p.dV : p.dK) + orow * DH + DQ * cq;
-        const float f = (m == 0) ? 1.f : p.scale;
+        const float f = (m == 0 ? 1.f : p.scale) * P_UNSCALE;
         // dK: map 2's half starts 64 columns on (d = 64: its own columns of a full-width product)
         const uint32_t col = s_addr - S_COL - 32 * cq + DQ * cq +
                              (m == 0 ? DV_COL : DK_COL + (DH == 64 ? 64 * h : 0));
