@@ -208,10 +208,11 @@ def _qkv(Q, K, V, dtype=torch.bfloat16, names=("Q", "K", "V")):
     B, Hq, Lq, d = Q.shape
     dev = Q.device
     _need(K, names[1], dtype, device=dev)
-    if K.dim() != 4 or int(K.shape[0]) != B or int(K.shape[3]) != d:
-        raise ValueError(f"{names[1]} must be [{B}, Hkv, Lk, {d}], got {tuple(K.shape)}")
-    _need(V, names[2], dtype, tuple(K.shape), dev)
-    Hkv, Lk = int(K.shape[1]), int(K.shape[2])
+    kv = K.shape
+    if len(kv) != 4 or kv[0] != B or kv[3] != d:
+        raise ValueError(f"{names[1]} must be [{B}, Hkv, Lk, {d}], got {tuple(kv)}")
+    _need(V, names[2], dtype, kv, dev)
+    Hkv, Lk = kv[1], kv[2]
     _heads(Hq, Hkv)
     return B, Hq, Hkv, Lq, Lk, d, dev
 
@@ -494,10 +495,11 @@ def _decode_args(Q, Kc, Vc, k_lens, O, lse, kv_names=("Kcache", "Vcache")):
     B, Hq, _, d = Q.shape
     dev = Q.device
     _need(Kc, kv_names[0], torch.bfloat16, device=dev)
-    if Kc.dim() != 4 or int(Kc.shape[3]) != d:
-        raise ValueError(f"{kv_names[0]} must be [*, Hkv, *, {d}], got {tuple(Kc.shape)}")
-    _need(Vc, kv_names[1], torch.bfloat16, tuple(Kc.shape), dev)
-    Hkv = int(Kc.shape[1])
+    kv = Kc.shape
+    if len(kv) != 4 or kv[3] != d:
+        raise ValueError(f"{kv_names[0]} must be [*, Hkv, *, {d}], got {tuple(kv)}")
+    _need(Vc, kv_names[1], torch.bfloat16, kv, dev)
+    Hkv = kv[1]
     _heads(Hq, Hkv)
     _klens(k_lens, B, dev, required=True)
     _opt(O, "O", torch.bfloat16, (B, Hq, 1, d), dev)
@@ -675,7 +677,7 @@ def attn_fwd_diff(Q, K, V, lam, scale=None, causal=False, k_lens=None, O=None, O
         o2 = torch.empty_like(Q) if want_aux and O2 is None else O2
         ls = lse
         if want_aux and ls is None:
-            ls = torch.empty((B, Hq, 2, Lq), dtype=torch.float32, device=dev)
+            ls = lam.new_empty((B, Hq, 2, Lq))
         _check(lib().attn_fwd_diff(Q.data_ptr(), K.data_ptr(), V.data_ptr(), lam.data_ptr(), n_lam,
                                    o.data_ptr(), _addr(o2), _addr(ls), B, Hq, Hkv, Lq, Lk, d,
                                    scale, _mask(causal), _addr(k_lens), ws.data_ptr(), ws.numel(),
@@ -714,7 +716,7 @@ def attn_bwd_diff(Q, K, V, lam, O, O2, dO, lse, scale=None, causal=False, k_lens
         dq = torch.empty_like(Q) if dQ is None else dQ
         dk = torch.empty_like(K) if dK is None else dK
         dv = torch.empty_like(V) if dV is None else dV
-        dl = torch.empty(n_lam, dtype=torch.bfloat16, device=dev) if dlam is None else dlam
+        dl = Q.new_empty(n_lam) if dlam is None else dlam
         _check(lib().attn_bwd_diff(Q.data_ptr(), K.data_ptr(), V.data_ptr(), lam.data_ptr(), n_lam,
                                    O.data_ptr(), O2.data_ptr(), dO.data_ptr(), lse.data_ptr(),
                                    dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dl.data_ptr(), B,
@@ -756,7 +758,7 @@ def _decode_diff(Q, Kc, Vc, block_table, lam, k_lens, scale, O, lse, workspace, 
         o = torch.empty_like(Q) if O is None else O
         ls = lse
         if ls is None and want_lse:
-            ls = torch.empty((B, Hq, 2), dtype=torch.float32, device=dev)
+            ls = lam.new_empty((B, Hq, 2))
         tail = (d, scale, k_lens.data_ptr(), ws.data_ptr(), ws.numel(), handle)
         if paged:
             _check(lib().attn_fwd_splitkv_decode_diff_paged(
