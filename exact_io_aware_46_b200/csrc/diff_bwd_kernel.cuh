@@ -41,7 +41,8 @@
 //
 // Measured on B200 (causal B2 H16 L8192 d128): dQ staged in the dS buffers and one tile
 // at a time 2715 us; dQ by reductions 2392; halves in turn 2031; fewer waits and no
-// divisions 1869; P_2 and dS in one go 1672; dK_1 by TS 1637.  What bounds it now is
+// divisions 1869; P_2 and dS in one go 1672; dK_1 by TS 1637; set-up overlapped with the
+// kernel before 1601; P_1 kept as scaled fp16 1638 (for its precision).  What bounds it now is
 // shared memory: the products read 416 KB of operands per 128-row tile (an SS product at
 // N = 64 is fed at ~95 of the 128 bytes a cycle), the copies in, the dS and the statistics'
 // broadcasts take another 190 KB, about 4700 of the ~6300 cycles of a tile.
@@ -953,8 +954,9 @@ struct Args : attn_bwd_impl::Args {
 // the causal mask's unequal items, leave SMs idle behind the longest one.  In units of a
 // tile, a part costs about one more (its K, V, first products and sums); the makespan
 // is the larger of the mean load and the longest part, and the least estimate wins.
-// Measured on B200: B3 Hq16 Hkv4 L1999 d64 (192 items of up to 64 tiles) 1 part 207 us,
-// 2 parts see the table of the backward in the design notes.
+// Measured on B200 (1 part / this rule's parts, us): causal B1 Hq32 Hkv1 L4096 d128 3181 / 454,
+// causal B1 Hq16 Hkv2 L8192 d128 1634 / 875, B1 Hq8 Hkv2 L2048 d128 212 / 72, B1 H4 L2048
+// d128 63 / 42, causal B3 Hq16 Hkv4 L1999 d64 197 / 192 (4 parts would be 185).
 inline int n_split(int B, int Hq, int Hkv, int Lq, int Lk, bool causal) {
   constexpr double SMS = 148.;
   const double items = static_cast<double>(B) * Hkv * ((Lk + BN - 1) / BN);

@@ -198,7 +198,8 @@ attn_status_t attn_bwd_sliding(const attn_bf16_t* Q, const attn_bf16_t* K, const
  *   O   = O_1 - lam[h] O_2,   lse[b,h,m,i] = log-sum-exp of row i of map m.
  * The customary scale is 1/sqrt(d / 2).
  *
- *   lam: device fp32 [n_lam], n_lam = 1 (one weight for all heads) or Hq.
+ *   lam: device fp32 [n_lam], n_lam = 1 (one weight for all heads) or Hq; like
+ *   dlam below it may be a slice of a larger tensor (aligned to its type only).
  *   O [B,Hq,Lq,d] bf16.  O2 [B,Hq,Lq,d] bf16 (O_2, for the backward; may be
  *   NULL).  lse [B,Hq,2,Lq] fp32 (may be NULL).  d = 64 or 128.  The other
  *   arguments, masks and errors as attn_fwd; a row that sees no key gets O = 0,
@@ -353,7 +354,9 @@ attn_status_t attn_fwd_splitkv_decode_diff_paged(
  *   k_lens[b] - n_b ... k_lens[b] - 1.
  *   Kpages, Vpages, block_table, max_blocks, page_size, n_pages: the cache, as
  *   attn_fwd_splitkv_decode_paged.  Pages and rows that take no token keep their
- *   contents; two sequences must not append to the same page.
+ *   contents (the differential decode may find anything there; the plain one,
+ *   which reads whole 128-row blocks, wants finite values, so allocate its pages
+ *   zeroed); two sequences must not append to the same page.
  *   Rotation: each of a head row's `maps` parts (1, or 2 for differential heads)
  *   of d / maps elements is rotated by itself, its first rope_dim elements in
  *   pairs (i, i + rope_dim / 2), or (2 i, 2 i + 1) with interleaved = 1:
