@@ -483,7 +483,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       if (h >= ncol) break;
       const float ls = rs[h] + rs[NH + h] + rs[2 * NH + h] + rs[3 * NH + h];
       const size_t ph = part_slot(h);
-      const bool has = live && ls > 0.f;
+      // (differential: a sum that is not a number stays, so that it reaches the result)
+      const bool has = live && (DIFF ? ls != 0.f : ls > 0.f);
       if (r < D) p.part_o[ph * D + r] = has ? __uint_as_float(o[h]) / ls : 0.f;
       if (r == 0) p.part_lse[ph] = has ? m_use[h] + log2f(ls) : -INFINITY;
     }
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(32 * DC_WARPS) diff_combine_kernel(const DiffC
     wsum_s[m] = ws;
     if (p.lse)
       p.lse[static_cast<size_t>(bh) * 2 + m] =
-          ws > 0.f ? (M + log2f(ws)) * 0.69314718055994531f : -INFINITY;
+          ws != 0.f ? (M + log2f(ws)) * 0.69314718055994531f : -INFINITY;
   }
   __syncthreads();
   if (threadIdx.x < D) {
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(32 * DC_WARPS) diff_combine_kernel(const DiffC
     for (int k = 0; k < DC_WARPS; ++k) o[k & 1] += acc_s[k][threadIdx.x];
     // (a map without a key has a sum of zero; both maps see the same keys)
     p.O[static_cast<size_t>(bh) * D + threadIdx.x] = __float2bfloat16_rn(
-        wsum_s[0] > 0.f && wsum_s[1] > 0.f ? o[0] / wsum_s[0] - lam * (o[1] / wsum_s[1]) : 0.f);
+        wsum_s[0] != 0.f && wsum_s[1] != 0.f ? o[0] / wsum_s[0] - lam * (o[1] / wsum_s[1]) : 0.f);
   }
 }
 

@@ -830,15 +830,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         constexpr int DQ = D / 4;  // columns this thread combines
         const int cq = (t * 2 + hf) * DQ;
         float* lx = lsum_x + (e_cnt & 1) * 4 * BM;
-        // a row that saw no key has a sum of exponentials' floors: its maximum tells
-        if (m_use == -INFINITY) l = 0.f;
+        // a row that saw no key has a sum of exponentials' floors: its maximum tells (a sum
+        // that is not a number stays: a NaN in the row's inputs is one in its results)
+        if (m_use == -INFINITY && l == l) l = 0.f;
         lx[(t * 2 + hf) * BM + r] = l;
         __syncwarp();
         if (sm100::lane_id() == 0) sm100::mbar_arrive(&l_bar[qd]);
         if (!(ok = sm100::mbar_wait(&l_bar[qd], e_cnt & 1, abort_flag, p.status))) break;
         ++e_cnt;
         const float l0 = lx[r] + lx[BM + r], l1 = lx[2 * BM + r] + lx[3 * BM + r];
-        const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
+        const float i0 = l0 != 0.f ? 1.f / l0 : 0.f, i1 = l1 != 0.f ? 1.f / l1 : 0.f;
         const float lam = __ldg(p.lam + (p.n_lam == 1 ? 0 : it.h));
         const size_t rix = (static_cast<size_t>(it.b) * p.Hq + it.h) * p.Lq + (live ? row : 0);
         const bool wide = ((reinterpret_cast<uintptr_t>(p.O) |
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           }
         };
-        const bool any = n_t > 0 && l0 > 0.f;  // the row sees a key (both maps see the same)
+        const bool any = n_t > 0 && l0 != 0.f;  // the row sees a key (both maps see the same)
 #pragma unroll 1
         for (int c = cq; c < cq + DQ; c += 16) {
           uint32_t o0[16], o1[16];
@@ -882,7 +883,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (p.lse && hf == 0) {
             const float lt = t ? l1 : l0;
             p.lse[((static_cast<size_t>(it.b) * p.Hq + it.h) * 2 + t) * p.Lq + row] =
-                lt > 0.f ? (m_use + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+                lt != 0.f ? (m_use + log2f(lt)) * 0.69314718055994531f : -INFINITY;
           }
         }
         sm100::tc_fence_before();

@@ -133,3 +133,32 @@ def test_a_shared_weight_trains_like_copies_of_it():
     a, b = out[0][6].double().sum().item(), out[1][6].double()
     # each of the eight is rounded once to bf16, the shared one too
     assert math.isclose(a, b.sum().item(), rel_tol=0, abs_tol=2 ** -8 * (b.abs().sum().item() + abs(a)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_row_that_is_not_a_number_stays_one(d):
+    """A NaN in a query row is a NaN in that row's results, and in no other row's; a row that sees
+    no key still gets zeros."""
+    attn = _lib()
+    Q, K, V, _, lam = (t.cuda() for t in problem(2, 4, 2, 150, 140, d, 71))
+    want = attn.attn_fwd_diff(Q, K, V, lam, causal=True)
+    bad = Q.clone()
+    bad[1, 2, [3, 40, 149]] = math.nan  # row 3 sees no key (150 queries, 140 keys)
+    O, O2, L = attn.attn_fwd_diff(bad, K, V, lam, causal=True)
+    hit = torch.zeros(2, 4, 150, dtype=torch.bool, device="cuda")
+    hit[1, 2, [40, 149]] = True
+    for got, ref_ in ((O, want[0]), (O2, want[1])):
+        assert got[hit].isnan().all() and torch.equal(got[~hit], ref_[~hit])
+    lh = hit[:, :, None].expand(2, 4, 2, 150)
+    assert L[lh].isnan().all() and torch.equal(L[~lh], want[2][~lh])
+    assert (O[:, :, :10] == 0).all() and (L[..., :10] == -math.inf).all()
+
+    lens = torch.tensor([140, 77], dtype=I32, device="cuda")
+    q = Q[:, :, -1:].contiguous()
+    want = attn.attn_fwd_splitkv_decode_diff(q, K, V, lam, lens)
+    q[1, 3] = math.nan
+    O, L = attn.attn_fwd_splitkv_decode_diff(q, K, V, lam, lens)
+    hit = torch.zeros(2, 4, dtype=torch.bool, device="cuda")
+    hit[1, 3] = True
+    assert O[hit].isnan().all() and torch.equal(O[~hit], want[0][~hit])
+    assert L[hit].isnan().all() and torch.equal(L[~hit], want[1][~hit])
