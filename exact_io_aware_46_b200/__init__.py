@@ -628,10 +628,19 @@ except ImportError:
     pass
 
 
-def _new_workspace(nbytes, dev, handle):
-    ws = torch.empty(max(256, int(nbytes)), dtype=torch.uint8, device=dev)
-    _check(lib().attn_clear_device_status(ws.data_ptr(), handle), "attn_clear_device_status")
-    return ws
+def _own_workspace(like, nbytes, handle, clear):
+    """A workspace for one call, from a bf16 tensor on its device: (tensor, bytes).  Nobody reads
+    its status word, so it is cleared only where the call needs its counters at zero."""
+    ws = like.new_empty(nbytes // 2)
+    if clear:
+        _check(lib().attn_clear_device_status(ws.data_ptr(), handle), "attn_clear_device_status")
+    return ws, nbytes
+
+
+@functools.lru_cache(maxsize=None)
+def _sms(index):
+    with torch.cuda.device(index):
+        return attn_num_sms()
 
 
 def _lam(lam, Hq, dev):
@@ -672,7 +681,8 @@ def attn_fwd_diff(Q, K, V, lam, scale=None, causal=False, k_lens=None, O=None, O
     scale = 1.0 / math.sqrt(d / 2) if scale is None else float(scale)
 
     def call(handle):
-        ws = _new_workspace(nbytes, dev, handle) if workspace is None else workspace
+        ws, room = (workspace, workspace.numel()) if workspace is not None else _own_workspace(
+            Q, nbytes, handle, B * Hq * ((Lq + 127) // 128) > _sms(dev.index))
         o = torch.empty_like(Q) if O is None else O
         o2 = torch.empty_like(Q) if want_aux and O2 is None else O2
         ls = lse
@@ -680,7 +690,7 @@ def attn_fwd_diff(Q, K, V, lam, scale=None, causal=False, k_lens=None, O=None, O
             ls = lam.new_empty((B, Hq, 2, Lq))
         _check(lib().attn_fwd_diff(Q.data_ptr(), K.data_ptr(), V.data_ptr(), lam.data_ptr(), n_lam,
                                    o.data_ptr(), _addr(o2), _addr(ls), B, Hq, Hkv, Lq, Lk, d,
-                                   scale, _mask(causal), _addr(k_lens), ws.data_ptr(), ws.numel(),
+                                   scale, _mask(causal), _addr(k_lens), ws.data_ptr(), room,
                                    handle), "attn_fwd_diff")
         return o, o2, ls
 
@@ -712,7 +722,8 @@ def attn_bwd_diff(Q, K, V, lam, O, O2, dO, lse, scale=None, causal=False, k_lens
     scale = 1.0 / math.sqrt(d / 2) if scale is None else float(scale)
 
     def call(handle):
-        ws = _new_workspace(nbytes, dev, handle) if workspace is None else workspace
+        ws, room = (workspace, workspace.numel()) if workspace is not None else _own_workspace(
+            Q, nbytes, handle, Lq == 0)
         dq = torch.empty_like(Q) if dQ is None else dQ
         dk = torch.empty_like(K) if dK is None else dK
         dv = torch.empty_like(V) if dV is None else dV
@@ -721,7 +732,7 @@ def attn_bwd_diff(Q, K, V, lam, O, O2, dO, lse, scale=None, causal=False, k_lens
                                    O.data_ptr(), O2.data_ptr(), dO.data_ptr(), lse.data_ptr(),
                                    dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dl.data_ptr(), B,
                                    Hq, Hkv, Lq, Lk, d, scale, _mask(causal), _addr(k_lens),
-                                   ws.data_ptr(), ws.numel(), handle), "attn_bwd_diff")
+                                   ws.data_ptr(), room, handle), "attn_bwd_diff")
         return dq, dk, dv, dl
 
     return _launch(dev, stream, call)
@@ -754,12 +765,13 @@ def _decode_diff(Q, Kc, Vc, block_table, lam, k_lens, scale, O, lse, workspace, 
     scale = 1.0 / math.sqrt(d / 2) if scale is None else float(scale)
 
     def call(handle):
-        ws = _new_workspace(nbytes, dev, handle) if workspace is None else workspace
+        ws, room = (workspace, workspace.numel()) if workspace is not None else _own_workspace(
+            Q, nbytes, handle, False)
         o = torch.empty_like(Q) if O is None else O
         ls = lse
         if ls is None and want_lse:
             ls = lam.new_empty((B, Hq, 2))
-        tail = (d, scale, k_lens.data_ptr(), ws.data_ptr(), ws.numel(), handle)
+        tail = (d, scale, k_lens.data_ptr(), ws.data_ptr(), room, handle)
         if paged:
             _check(lib().attn_fwd_splitkv_decode_diff_paged(
                 Q.data_ptr(), Kc.data_ptr(), Vc.data_ptr(), block_table.data_ptr(), max_blocks,
@@ -850,7 +862,7 @@ def attn_kv_append_paged(K, V, Kp, Vp, block_table, k_lens, cu_seqlens=None, Q=N
         raise ValueError(f"Kpages must be [n_pages, Hkv, page, d], got {tuple(Kp.shape)}")
     n_pages, Hkv, page, d = Kp.shape
     dev = Kp.device
-    _need(Vp, "Vpages", torch.bfloat16, (n_pages, Hkv, page, d), dev)
+    _need(Vp, "Vpages", torch.bfloat16, Kp.shape, dev)
     T, _, ks = _tokens(K, "K", d, dev, Hkv)
     _, _, vs = _tokens(V, "V", d, dev, Hkv, T)
     _need(k_lens, "k_lens", torch.int32, device=dev)
@@ -881,21 +893,22 @@ def attn_kv_append_paged(K, V, Kp, Vp, block_table, k_lens, cu_seqlens=None, Q=N
         if cos.dim() != 2:
             raise ValueError(f"cos must be [n_pos, rope_dim / 2], got {tuple(cos.shape)}")
         n_pos, rope = int(cos.shape[0]), 2 * int(cos.shape[1])
-        _need(sin, "sin", torch.float32, tuple(cos.shape), dev)
+        _need(sin, "sin", torch.float32, cos.shape, dev)
     nbytes = attn_kv_append_paged_workspace_size()
     if workspace is not None:
         _ws_check(workspace, nbytes, dev)
 
     def call(handle):
-        ws = _new_workspace(nbytes, dev, handle) if workspace is None else workspace
+        ws, room = (workspace, workspace.numel()) if workspace is not None else _own_workspace(
+            Kp, nbytes, handle, False)
         qo = Q_out
         if Q is not None and qo is None:
-            qo = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+            qo = Kp.new_empty((T, Hq, d))
         _check(lib().attn_kv_append_paged(
             _addr(Q), qs, K.data_ptr(), ks, V.data_ptr(), vs, _addr(qo), Kp.data_ptr(),
             Vp.data_ptr(), block_table.data_ptr(), block_table.shape[1], page, n_pages,
             _addr(cu_seqlens), k_lens.data_ptr(), B, T, Hq, Hkv, d, _addr(cos), _addr(sin), n_pos,
-            rope, maps, 1 if interleaved else 0, ws.data_ptr(), ws.numel(), handle),
+            rope, maps, 1 if interleaved else 0, ws.data_ptr(), room, handle),
             "attn_kv_append_paged")
         return qo
 

@@ -192,14 +192,16 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, const uint32_t (&w)[4]
 // ------------------------------------------------------------------ prep
 
 // D_1, D_2, the log2-LSEs and a zeroed accumulator row of every (padded) query row: DH / 8
-// lanes a row, sixteen bytes each of O, O2 and dO.
+// lanes a row, sixteen bytes each of O, O2 and dO.  And zeroed scheduler counters, so that
+// a call with query rows works on any workspace.
 template <int DH>
 __global__ void __launch_bounds__(256)
     prep_kernel(const __nv_bfloat16* O, const __nv_bfloat16* O2, const __nv_bfloat16* dO,
                 const float* lse, const float* lam, int n_lam, float* dq_acc, float* stats,
-                long long rows, int Hq, int Lq, int Lqp) {
+                int* sched, long long rows, int Hq, int Lq, int Lqp) {
   constexpr int LPR = DH / 8;  // lanes per row
   sm100::grid_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x < 2) sched[threadIdx.x] = 0;
   const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
   const int lane = threadIdx.x % LPR;
   if (row >= rows) return;  // whole rows, and rows is a multiple of 128: whole warps
@@ -1037,7 +1039,7 @@ attn_status_t launch_d(const Args& a, cudaStream_t s) {
   if (a.Lq > 0) {
     const long long rows = BH * p.Lqp;
     prep_kernel<DH><<<static_cast<unsigned>((rows * (DH / 8) + 255) / 256), 256, 0, s>>>(
-        a.O, a.O2, a.dO, a.lse, a.lam, a.n_lam, p.dq_acc, stats, rows, a.Hq, a.Lq, p.Lqp);
+        a.O, a.O2, a.dO, a.lse, a.lam, a.n_lam, p.dq_acc, stats, p.sched, rows, a.Hq, a.Lq, p.Lqp);
     if (attn_host::report_launch(prep_kernel<DH>, "diff prep_kernel") != cudaSuccess)
       return ATTN_ERR_CUDA;
   }

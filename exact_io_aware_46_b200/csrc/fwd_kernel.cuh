@@ -427,8 +427,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (uint32_t k = 0;; ++k) {
         if (!sm100::mbar_wait(&item_empty[k % NI], ((k / NI) & 1) ^ 1, abort_flag, p.status))
           break;
-        int w = (k == 0) ? static_cast<int>(blockIdx.x)
-                         : atomicAdd(p.sched, 1) + static_cast<int>(gridDim.x);
+        int w = static_cast<int>(blockIdx.x);
+        if (MODE == MODE_DIFF && k > 0 && p.n_items <= static_cast<int>(gridDim.x))
+          w = -1;  // an item a CTA: the counters are not used (a small call need not clear them)
+        else if (k > 0)
+          w = atomicAdd(p.sched, 1) + static_cast<int>(gridDim.x);
         if (w >= p.n_items) w = -1;
         *reinterpret_cast<volatile int*>(&item_ring[k % NI]) = w;
         sm100::mbar_arrive(&item_full[k % NI]);

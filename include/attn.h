@@ -205,7 +205,9 @@ attn_status_t attn_bwd_sliding(const attn_bf16_t* Q, const attn_bf16_t* K, const
  *   arguments, masks and errors as attn_fwd; a row that sees no key gets O = 0,
  *   O2 = 0 and both lse = -inf.  K and V rows at and past k_lens[b] are not used
  *   and may hold anything.  More than 2^30 128-row tiles over all heads return
- *   ATTN_ERR_UNSUPPORTED.
+ *   ATTN_ERR_UNSUPPORTED.  A call of at most attn_num_sms() query tiles
+ *   (B * Hq * ceil(Lq / 128)) uses no counter of the workspace: it need only be
+ *   cleared beforehand if its status word is to be read.
  */
 size_t attn_fwd_diff_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk, int d);
 attn_status_t attn_fwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const attn_bf16_t* V,
@@ -226,7 +228,8 @@ attn_status_t attn_fwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const at
  *   fp32 statistics per query row, the partial sums of dlam and, where there are
  *   few key/value heads and keys, fp32 partial sums of dV and dK.  dQ's sums are
  *   formed in no fixed order (its last bit may differ from run to run); dK, dV and
- *   dlam are the same each time.
+ *   dlam are the same each time.  With Lq > 0 the workspace's counters are set by
+ *   the call itself, so it, too, need only be cleared for its status word.
  */
 size_t attn_bwd_diff_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk, int d);
 attn_status_t attn_bwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const attn_bf16_t* V,
@@ -322,7 +325,8 @@ attn_status_t attn_fwd_splitkv_decode_paged(const attn_bf16_t* Q, const attn_bf1
  *   most 8 (any number); the split length goes by B, Hkv and the cache's
  *   capacity, so the workspace is attn_decode_diff_workspace_size(B, Hq, Hkv,
  *   Lmax, d) bytes (Lmax = max_blocks * page_size for a paged cache).
- * Cache rows at and past k_lens[b] are not used and may hold anything.
+ * Cache rows at and past k_lens[b] are not used and may hold anything.  The
+ * workspace need only be cleared beforehand if its status word is to be read.
  */
 size_t attn_decode_diff_workspace_size(int B, int Hq, int Hkv, int Lmax, int d);
 attn_status_t attn_fwd_splitkv_decode_diff(const attn_bf16_t* Q, const attn_bf16_t* Kcache,
@@ -368,6 +372,7 @@ attn_status_t attn_fwd_splitkv_decode_diff_paged(
  *   below n_b or above the cache's capacity, or a row past n_pos, sets
  *   ATTN_DEV_BAD_KLEN; a block-table entry outside [0, n_pages) sets
  *   ATTN_DEV_BAD_PAGE.  The tokens concerned write nothing, Q_out included.
+ *   Only the workspace's status word is used; clear it beforehand to read it.
  */
 size_t attn_kv_append_paged_workspace_size(void);
 attn_status_t attn_kv_append_paged(const attn_bf16_t* Q, long long q_stride, const attn_bf16_t* K,

@@ -162,3 +162,41 @@ def test_a_row_that_is_not_a_number_stays_one(d):
     hit[1, 3] = True
     assert O[hit].isnan().all() and torch.equal(O[~hit], want[0][~hit])
     assert L[hit].isnan().all() and torch.equal(L[~hit], want[1][~hit])
+
+
+@pytest.mark.parametrize("fill", [0x7F, 0x80, 0xFF])
+@pytest.mark.parametrize("extra", [0, 1])
+def test_calls_need_no_cleared_workspace_but_for_its_status(fill, extra):
+    """As many query tiles as SMs, and one more: on memory that holds anything, the calls that may
+    go without clearing give what they give on cleared workspaces."""
+    attn = _lib()
+    B, Hq, L, d = 1, attn.attn_num_sms() + extra, 128, 64
+    Q, K, V, dO, lam = (t.cuda() for t in problem(B, Hq, Hq, L, L, d, 81))
+    lens = torch.tensor([L], dtype=I32, device="cuda")
+    kp, vp, table = K.clone(), V.clone(), torch.zeros(1, 1, dtype=I32, device="cuda")
+    tok = Q[0, :, :1].transpose(0, 1).contiguous()
+
+    def run(ws):
+        O, O2, lse = attn.attn_fwd_diff(Q, K, V, lam, workspace=ws(attn.attn_fwd_diff_workspace_size(
+            B, Hq, Hq, L, L, d), extra == 0))
+        out = (O, O2, lse) + attn.attn_bwd_diff(Q, K, V, lam, O, O2, dO, lse, workspace=ws(
+            attn.attn_bwd_diff_workspace_size(B, Hq, Hq, L, L, d), True))
+        qr = attn.attn_kv_append_paged(tok, tok, kp, vp, table, lens, Q=tok, workspace=ws(
+            attn.attn_kv_append_paged_workspace_size(), True))
+        return out + (qr, kp) + attn.attn_fwd_splitkv_decode_diff(
+            qr.view(B, Hq, 1, d), kp, vp, lam, lens, workspace=ws(
+                attn.attn_decode_diff_workspace_size(B, Hq, Hq, L, d), True))
+
+    what = ("O", "O2", "lse", "dQ", "dK", "dV", "dlam", "q", "pages", "dO", "dlse")
+
+    def any_memory(n, may):
+        return torch.full((n,), fill if may else 0, dtype=torch.uint8, device="cuda")
+
+    want = run(lambda n, may: torch.zeros(n, dtype=torch.uint8, device="cuda"))
+    for _ in range(3):
+        _like(run(any_memory), want, what)
+    # the binding's own workspaces, handed out where a filled block was
+    for _ in range(3):
+        for n in (256, 1 << 16, 1 << 20, 1 << 23):
+            torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        _like(run(lambda n, may: None), want, what)
