@@ -274,10 +274,11 @@ __device__ __forceinline__ constexpr bool poly_pair(int cp) {
 }
 
 // Differential heads: a quarter at either width (causal B4 H16 L4096 d128: none 461 us, an eighth
-// 442, a quarter 434, three eighths 455), by the degree-4 polynomial without the
+// 442, a quarter 434, three eighths 455; every fourth pair 422 against two of eight 426, after
+// the product with V was put in two parts), by the degree-4 polynomial without the
 // zeroing of masked entries, which costs less than the zeroing saved (440 us with the
 // degree-3 form above) and keeps the log-sum-exp to 1e-6.
-__device__ __forceinline__ constexpr bool diff_poly_pair(int cp) { return (cp & 7) >= 6; }
+__device__ __forceinline__ constexpr bool diff_poly_pair(int cp) { return (cp & 3) == 3; }
 
 // S_t = Q_t K_j^T: 128 x 128 (keys) x D, both operands K-major SW128 panels.
 // One base descriptor per operand; the K-steps (32 bytes each: 16 bf16 or 32
@@ -335,6 +336,24 @@ __device__ __forceinline__ void issue_pv_tile(uint32_t o_tmem, uint32_t p_tmem, 
   }
 }
 
+// The instructions of issue_pv_tile (bf16) for the first (part 0) or the last 32 keys
+// of either 64-key half.  Differential heads: the first part runs beside the exponentials
+// of the last, which shortens the chain S -> P -> O -> S (causal B4 H16 L4096: d128 432 -> 422
+// us, d64 402 -> 391; 48 and 16 keys instead 429 and 397).
+template <int D>
+__device__ __forceinline__ void issue_pv_part(uint32_t o_tmem, uint32_t p_tmem, uint32_t v_smem,
+                                              bool acc, int part) {
+  using C = Cfg<D, 2>;
+  const uint64_t vd = sm100::sdesc_sw128(v_smem, CHUNK_BYTES, 1024);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = 4 * (i >> 1) + 2 * part + (i & 1);  // 16 keys each
+    sm100::mma_ts(o_tmem, p_tmem + (k >> 2) * C::P_HALF + (k & 3) * 8,
+                  vd + static_cast<uint64_t>((k * 16 * 128) >> 4), C::IDESC_PV,
+                  (acc || i > 0) ? 1u : 0u);
+  }
+}
+
 template <int D, int MODE>
 __global__ void __launch_bounds__(NTHREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -368,6 +387,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   // differential: the row sums of a lane quarter's four warps are in ([4]; a bounded wait,
   // unlike a named barrier)
   uint64_t* l_bar = bars + 56;
+  uint64_t* p_half = bars + 60;  // [2]: the first 32 keys of either half of P_t are in
+  static_assert(2 * C::NS + 15 + 2 * NI + (NI + 3) / 2 <= 56, "barrier area");
 
   const int warp = threadIdx.x >> 5;
 
@@ -388,8 +409,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       sm100::mbar_init(&p_free[t], 1);
     }
     sm100::mbar_init(drain, 1);
-    if constexpr (MODE == MODE_DIFF)
+    if constexpr (MODE == MODE_DIFF) {
       for (int i = 0; i < 4; ++i) sm100::mbar_init(&l_bar[i], 4);
+      for (int t = 0; t < 2; ++t) sm100::mbar_init(&p_half[t], NSMX / 2);
+    }
     for (int i = 0; i < NI; ++i) {
       sm100::mbar_init(&item_full[i], 1);
       sm100::mbar_init(&item_empty[i], 1 + 32 * NSMX);  // the MMA thread + all softmax threads
@@ -587,10 +610,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               if (lo[t] <= j && j < n_t) {
                 if (j == lo[t] && !sm100::mbar_wait(&o_empty[t], oe_par, abort_flag, p.status))
                   return false;
+                auto part = [&](int i) {
+                  if (leader)
+                    issue_pv_part<D>(tmem + C::o_col(t), tmem + C::p_col(t),
+                                     kv_addr + vs * C::TILE_BYTES, i > 0 || j > lo[t], i);
+                };
+                if constexpr (MODE == MODE_DIFF) {
+                  if (!sm100::mbar_wait(&p_half[t], pc & 1, abort_flag, p.status)) return false;
+                  sm100::tc_fence_after();
+                  part(0);
+                }
                 if (!sm100::mbar_wait(&p_full[t], pc & 1, abort_flag, p.status)) return false;
                 ++pc;
                 sm100::tc_fence_after();
-                issue_pv(t, vs, j > lo[t]);
+                if constexpr (MODE == MODE_DIFF) part(1);
+                else issue_pv(t, vs, j > lo[t]);
                 if constexpr (C::SEP_P) commit(&p_free[t]);
                 if (j == n_t - 1) commit(&o_full[t]);
               }
@@ -803,6 +837,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               s[cp] = sm100::pack_bf16x2(e.x, e.y);
             }
             sm100::tmem_st16(pw_addr + 16 * q, &s[16 * q]);
+            if (MODE == MODE_DIFF && q == 0) {
+              sm100::tmem_st_wait();
+              sm100::tc_fence_before();
+              __syncwarp();
+              if (sm100::lane_id() == 0) sm100::mbar_arrive(&p_half[t]);
+            }
           }
         } else {
 #pragma unroll
