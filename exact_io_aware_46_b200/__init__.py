@@ -39,6 +39,11 @@ import threading
 
 import torch
 
+try:  # checks and marshalling of the differential calls' common form, compiled
+    from . import _binding
+except ImportError:  # not built: the same in Python
+    _binding = None
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libattn.so")
 
@@ -114,6 +119,14 @@ class AttnError(RuntimeError):
         super().__init__(f"{where}: {status_string(code)} ({code})")
 
 
+#: the entry points that _binding calls, in the order that its bind() takes
+_BOUND = ("attn_fwd_diff", "attn_bwd_diff", "attn_fwd_splitkv_decode_diff",
+          "attn_fwd_splitkv_decode_diff_paged", "attn_kv_append_paged",
+          "attn_fwd_diff_workspace_size", "attn_bwd_diff_workspace_size",
+          "attn_decode_diff_workspace_size", "attn_kv_append_paged_workspace_size",
+          "attn_clear_device_status", "attn_num_sms")
+
+
 def lib() -> ctypes.CDLL:
     """The loaded C library; raises if it has not been built."""
     global _lib
@@ -130,6 +143,9 @@ def lib() -> ctypes.CDLL:
                 fn = getattr(L, name)
                 fn.restype = res
                 fn.argtypes = args
+            if _binding is not None:
+                _binding.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value
+                                for n in _BOUND))
             _lib = L
     return _lib
 
@@ -600,6 +616,17 @@ def attn_bwd(Q, K, V, O, dO, lse, scale=None, causal=False, k_lens=None, dQ=None
 # ------------------------------------------------------------------ differential attention
 
 
+# Each of these functions hands sound arguments to _binding, which answers None to anything
+# else (before any launch), to a stream argument, to another device than the current one and
+# before the library is loaded; the Python code after it is for those.
+
+
+def _done(result, where):
+    if type(result) is int:  # a status that is not a refusal
+        _check(result, where)
+    return result
+
+
 def _launch(dev, stream, call):
     """``call(handle)`` on ``stream`` (default: the current stream of the tensors' device):
     what it allocates belongs to that stream, and the tensors' device is current meanwhile."""
@@ -669,6 +696,11 @@ def attn_fwd_diff(Q, K, V, lam, scale=None, causal=False, k_lens=None, O=None, O
     1/sqrt(d / 2).  Returns (O, O2, LSE): O2 [B,Hq,Lq,d] bf16, the second map's output, and
     LSE fp32 [B,Hq,2,Lq] are what attn_bwd_diff needs (None if ``want_aux`` is False and they
     are not passed in)."""
+    if stream is None and _binding is not None:
+        done = _binding.fwd_diff(Q, K, V, lam, scale, causal, k_lens, O, O2, lse, workspace,
+                                 want_aux)
+        if done is not None:
+            return _done(done, "attn_fwd_diff")
     B, Hq, Hkv, Lq, Lk, d, dev = _qkv(Q, K, V)
     n_lam = _lam(lam, Hq, dev)
     _klens(k_lens, B, dev)
@@ -706,6 +738,11 @@ def attn_bwd_diff(Q, K, V, lam, O, O2, dO, lse, scale=None, causal=False, k_lens
                   dK=None, dV=None, dlam=None, workspace=None, stream=None):
     """Backward of attn_fwd_diff, from its O, O2 and LSE.  Returns (dQ, dK, dV, dlam), bf16
     like every gradient here; dlam has lam's shape (one shared weight gets the heads' sum)."""
+    if stream is None and _binding is not None:
+        done = _binding.bwd_diff(Q, K, V, lam, O, O2, dO, lse, scale, causal, k_lens, dQ, dK, dV,
+                                 dlam, workspace)
+        if done is not None:
+            return _done(done, "attn_bwd_diff")
     B, Hq, Hkv, Lq, Lk, d, dev = _qkv(Q, K, V)
     n_lam = _lam(lam, Hq, dev)
     for t, name in ((O, "O"), (O2, "O2"), (dO, "dO")):
@@ -740,6 +777,11 @@ def attn_bwd_diff(Q, K, V, lam, O, O2, dO, lse, scale=None, causal=False, k_lens
 
 def _decode_diff(Q, Kc, Vc, block_table, lam, k_lens, scale, O, lse, workspace, stream, want_lse):
     """Both differential decodes: contiguous cache (``block_table`` None) or pages."""
+    if stream is None and _binding is not None:
+        done = _binding.decode_diff(Q, Kc, Vc, block_table, lam, k_lens, scale, O, lse, workspace,
+                                    want_lse)
+        if done is not None:
+            return _done(done, "attn_fwd_splitkv_decode_diff")
     paged = block_table is not None
     names = ("Kpages", "Vpages") if paged else ("Kcache", "Vcache")
     B, Hq, Hkv, d, dev = _decode_args(Q, Kc, Vc, k_lens, O, None, names)
@@ -857,6 +899,11 @@ def attn_kv_append_paged(K, V, Kp, Vp, block_table, k_lens, cu_seqlens=None, Q=N
     [n_pos, rope_dim/2] or both None (no rotation); maps = 2 rotates each half of a
     differential head by itself.  Returns the rotated Q [T,Hq,d] (None without Q); rows behind
     the last sequence are left as they were."""
+    if stream is None and _binding is not None:
+        done = _binding.append(K, V, Kp, Vp, block_table, k_lens, cu_seqlens, Q, Q_out, cos, sin,
+                               maps, interleaved, workspace)
+        if done is not None:
+            return _done(done, "attn_kv_append_paged")[0]
     _need(Kp, "Kpages", torch.bfloat16)
     if Kp.dim() != 4:
         raise ValueError(f"Kpages must be [n_pages, Hkv, page, d], got {tuple(Kp.shape)}")

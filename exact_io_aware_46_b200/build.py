@@ -1,4 +1,5 @@
-"""Builds the CUDA library ``libattn.so`` in-tree with nvcc for sm_100a only."""
+"""Builds the CUDA library ``libattn.so`` (nvcc, sm_100a only) and the Python extension
+``_binding`` (g++, against torch's headers) in-tree."""
 
 from __future__ import annotations
 
@@ -6,12 +7,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SO = os.path.join(HERE, "libattn.so")
 SRC = os.path.join(HERE, "csrc", "attn_api.cu")
 SRC_NOALLOC = os.path.join(HERE, "csrc", "decode_noalloc.cu")
+BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+SRC_BINDING = os.path.join(HERE, "csrc", "binding.cpp")
 
 
 def nvcc() -> str:
@@ -26,15 +30,36 @@ def sources():
         os.path.join(ROOT, "include", "attn.h")]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(SO):
+def up_to_date(so: str, srcs) -> bool:
+    if not os.path.exists(so):
         return False
-    t = os.path.getmtime(SO)
-    return all(os.path.getmtime(s) <= t for s in sources())
+    t = os.path.getmtime(so)
+    return all(os.path.getmtime(s) <= t for s in srcs)
+
+
+def build_binding(force: bool = False) -> str:
+    if not force and up_to_date(BINDING, [SRC_BINDING, os.path.join(ROOT, "include", "attn.h")]):
+        return BINDING
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
+    inc = [os.path.join(ROOT, "include"), os.path.join(t, "include"),
+           os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    subprocess.check_call(
+        [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+        + ["-I" + i for i in inc] + [SRC_BINDING, "-o", tmp, "-L" + os.path.join(t, "lib")]
+        + ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"])
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    build_binding(force)
+    if not force and up_to_date(SO, sources()):
         return SO
     tmp = SO + f".tmp{os.getpid()}"
     cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
