@@ -22,6 +22,7 @@
 
 #include <cstdint>
 
+#include "launch_cache.cuh"
 #include "sm100.cuh"
 
 namespace attn_append_impl {
@@ -75,6 +76,8 @@ __device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
 
 template <int D>
 __global__ void __launch_bounds__(NTHREADS) append_kernel(const Params p) {
+  sm100::grid_launch_dependents();  // launches overlap; nothing is read or written before the wait
+  sm100::grid_wait();
   constexpr int UPR = D / 16;               // units per head row
   constexpr int LANES = NTHREADS / UPR;     // head rows a block handles at a time
   const int t = blockIdx.x;
@@ -236,8 +239,7 @@ cudaError_t launch_d(Params p, int sms, cudaStream_t s) {
   const int rows = p.q_rows + 2 * p.Hkv;
   p.rows_per_y = rows_per_block(p.T, rows, LANES, sms);
   const dim3 grid(p.T, (rows + p.rows_per_y - 1) / p.rows_per_y);
-  append_kernel<D><<<grid, NTHREADS, 0, s>>>(p);
-  return cudaGetLastError();
+  return attn_host::launch_overlapped(append_kernel<D>, grid, dim3(NTHREADS), 0, s, p);
 }
 
 inline cudaError_t launch(const Params& p, int d, int sms, cudaStream_t s) {

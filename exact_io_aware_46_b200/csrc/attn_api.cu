@@ -193,6 +193,12 @@ static attn_status_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, co
     e = set_smem(kernel, smem);
     if (e == cudaSuccess) kernel<<<grid, attn_fwd_impl::NTHREADS, smem, s>>>(tq, tk, tv, p);
   };
+  auto run_overlapped = [&](auto kernel, int smem) {
+    e = set_smem(kernel, smem);
+    if (e == cudaSuccess)
+      e = attn_host::launch_overlapped(kernel, dim3(grid), dim3(attn_fwd_impl::NTHREADS), smem, s,
+                                       tq, tk, tv, p);
+  };
   using namespace attn_fwd_impl;
   if (d == 128) {
     constexpr int smem = Cfg<128>::SMEM_BYTES;
@@ -200,7 +206,7 @@ static attn_status_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, co
     else if (mode == MODE_WINDOW) run(fwd_kernel<128, MODE_WINDOW>, smem);
     else if (mode == MODE_FP8) run(fwd_kernel<128, MODE_FP8>, Cfg<128, 1>::SMEM_BYTES);
     else if (mode == MODE_MERGE) run(fwd_kernel<128, MODE_MERGE>, smem);
-    else if (mode == MODE_DIFF) run(fwd_kernel<128, MODE_DIFF>, smem);
+    else if (mode == MODE_DIFF) run_overlapped(fwd_kernel<128, MODE_DIFF>, smem);
     else run(fwd_kernel<128, MODE_VARLEN>, smem);
   } else {
     if (mode == MODE_FP8) return ATTN_ERR_UNSUPPORTED;
@@ -208,7 +214,7 @@ static attn_status_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, co
     if (mode == MODE_PLAIN) run(fwd_kernel<64, MODE_PLAIN>, smem);
     else if (mode == MODE_WINDOW) run(fwd_kernel<64, MODE_WINDOW>, smem);
     else if (mode == MODE_MERGE) run(fwd_kernel<64, MODE_MERGE>, smem);
-    else if (mode == MODE_DIFF) run(fwd_kernel<64, MODE_DIFF>, smem);
+    else if (mode == MODE_DIFF) run_overlapped(fwd_kernel<64, MODE_DIFF>, smem);
     else run(fwd_kernel<64, MODE_VARLEN>, smem);
   }
   if (e != cudaSuccess) return ATTN_ERR_CUDA;

@@ -176,7 +176,15 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* red = reinterpret_cast<float*>(smem + OFF_RED);
 
-  if constexpr (DIFF) sm100::grid_launch_dependents();  // the combine's set-up
+  if constexpr (DIFF) {
+    if (threadIdx.x == 0) {
+      sm100::prefetch_tmap(&tmK);
+      sm100::prefetch_tmap(&tmV);
+    }
+    sm100::grid_wait();  // the launch and the above ran beside the end of the kernel before
+    // the combine's set-up; only now, as it reads the lengths before its own wait
+    sm100::grid_launch_dependents();
+  }
   // grid (sequence x kv head, chunk position counted from the sequence's end)
   const int hkv = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
   const int kl = valid_klen(p.k_lens, b, p.Lmax, p.status,
@@ -231,7 +239,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     *abort_flag = 0;
     sm100::fence_barrier_init();
   }
-  if (warp == 0 && sm100::lane_id() == 0) {
+  if (!DIFF && warp == 0 && sm100::lane_id() == 0) {
     sm100::prefetch_tmap(&tmK);
     sm100::prefetch_tmap(&tmV);
   }
@@ -578,6 +586,7 @@ __global__ void __launch_bounds__(32 * DC_WARPS) diff_combine_kernel(const DiffC
   constexpr int EPL = D / 32;
   __shared__ float acc_s[DC_WARPS][D];
   __shared__ float wsum_s[2];
+  sm100::grid_launch_dependents();
   const int bh = blockIdx.x, b = bh / p.Hq, h = bh % p.Hq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m = warp & 1;
@@ -668,8 +677,12 @@ cudaError_t launch_split(const SplitParams& sp, cudaStream_t s) {
   cudaError_t e = attn_host::report(attn_host::set_smem(kernel, tc::SMEM_BYTES),
                                     "decode tensor-core kernel shared-memory attribute");
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(static_cast<unsigned>(sp.Hkv * sp.B), sp.nsm, 1), tc::NTHREADS, tc::SMEM_BYTES,
-           s>>>(tk, tv, sp);
+  const dim3 grid(static_cast<unsigned>(sp.Hkv * sp.B), sp.nsm, 1);
+  if constexpr (DIFF)
+    return attn_host::report(
+        attn_host::launch_overlapped(kernel, grid, dim3(tc::NTHREADS), tc::SMEM_BYTES, s, tk, tv, sp),
+        "differential decode split kernel");
+  kernel<<<grid, tc::NTHREADS, tc::SMEM_BYTES, s>>>(tk, tv, sp);
   return attn_host::report_launch(kernel, "decode tensor-core split kernel");
 }
 

@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(256)
                 int* sched, long long rows, int Hq, int Lq, int Lqp) {
   constexpr int LPR = DH / 8;  // lanes per row
   sm100::grid_launch_dependents();
+  sm100::grid_wait();
   if (blockIdx.x == 0 && threadIdx.x < 2) sched[threadIdx.x] = 0;
   const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
   const int lane = threadIdx.x % LPR;
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(256)
                   float scale, long long conv_blocks, const float* lam_part, __nv_bfloat16* dlam,
                   int B, int Hq, int Hkv, int Lk, int n_lam, int n_split, const float* kv_part,
                   __nv_bfloat16* dK, __nv_bfloat16* dV) {
+  sm100::grid_launch_dependents();
   sm100::grid_wait();
   const int n_kv = (Lk + BN - 1) / BN;
   if (blockIdx.x >= conv_blocks + n_lam) {
@@ -1038,9 +1040,12 @@ attn_status_t launch_d(const Args& a, cudaStream_t s) {
 
   if (a.Lq > 0) {
     const long long rows = BH * p.Lqp;
-    prep_kernel<DH><<<static_cast<unsigned>((rows * (DH / 8) + 255) / 256), 256, 0, s>>>(
-        a.O, a.O2, a.dO, a.lse, a.lam, a.n_lam, p.dq_acc, stats, p.sched, rows, a.Hq, a.Lq, p.Lqp);
-    if (attn_host::report_launch(prep_kernel<DH>, "diff prep_kernel") != cudaSuccess)
+    const dim3 grid(static_cast<unsigned>((rows * (DH / 8) + 255) / 256));
+    if (attn_host::report(
+            attn_host::launch_overlapped(prep_kernel<DH>, grid, dim3(256), 0, s, a.O, a.O2, a.dO,
+                                         a.lse, a.lam, a.n_lam, p.dq_acc, stats, p.sched, rows, a.Hq,
+                                         a.Lq, p.Lqp),
+            "diff prep_kernel") != cudaSuccess)
       return ATTN_ERR_CUDA;
   }
   if (p.n_items > 0) {

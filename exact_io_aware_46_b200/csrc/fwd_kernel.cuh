@@ -433,6 +433,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   sm100::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (MODE == MODE_DIFF) {
+    // the set-up so far ran beside the end of the kernel before; the one behind may set up, too
+    // (not earlier: this block's tensor memory is its own by now)
+    sm100::grid_wait();
+    sm100::grid_launch_dependents();
+  }
 
   // consumers' view of the item ring: the k-th item index, or -1 at the end
   auto next_item = [&](uint32_t k, int& w) -> bool {
