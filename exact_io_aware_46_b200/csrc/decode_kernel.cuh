@@ -176,22 +176,56 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* red = reinterpret_cast<float*>(smem + OFF_RED);
 
-  if constexpr (DIFF) {
+  const int warp = threadIdx.x >> 5;
+  auto set_up = [&]() {
     if (threadIdx.x == 0) {
+      for (int i = 0; i < NSLOT; ++i) {
+        sm100::mbar_init(&kv_full[i], 1);
+        sm100::mbar_init(&kv_empty[i], 1);
+      }
+      sm100::mbar_init(s_full, 1);
+      sm100::mbar_init(p_full, 4);
+      sm100::mbar_init(o_full, 1);
+      sm100::mbar_init(q_ready, 4);
+      sm100::mbar_init(drain, 1);
+      sm100::mbar_init(&mx_bar[0], 4);
+      sm100::mbar_init(&mx_bar[1], 4);
+      sm100::mbar_init(sum_bar, 4);
+      *abort_flag = 0;
+      sm100::fence_barrier_init();
+    }
+    if (warp == 0 && sm100::lane_id() == 0) {
       sm100::prefetch_tmap(&tmK);
       sm100::prefetch_tmap(&tmV);
     }
-    sm100::grid_wait();  // the launch and the above ran beside the end of the kernel before
-    // the combine's set-up; only now, as it reads the lengths before its own wait
-    sm100::grid_launch_dependents();
+    if (warp == 1) {
+      sm100::tmem_alloc(tmem_slot, 32);
+      sm100::tmem_relinquish();
+    }
+    sm100::tc_fence_before();
+    __syncthreads();
+    sm100::tc_fence_after();
+  };
+  // Differential: the set-up runs beside the end of the kernel before (B1 Hkv8 d128 cache 4096:
+  // 9.8 -> 9.2 us of one decode after another; B16, whose blocks then share SMs less evenly,
+  // 37.1 -> 38.9)
+  if constexpr (DIFF) {
+    set_up();
+    sm100::grid_wait();
   }
+  auto leave = [&]() {  // a block without work
+    if (DIFF && warp == 1) sm100::tmem_dealloc(*tmem_slot, 32);
+  };
   // grid (sequence x kv head, chunk position counted from the sequence's end)
   const int hkv = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
   const int kl = valid_klen(p.k_lens, b, p.Lmax, p.status,
                             blockIdx.y == gridDim.y - 1 && hkv == 0 && threadIdx.x == 0);
   const int ch = DIFF ? p.ch : CH;
   const int chunk = (kl + ch - 1) / ch - static_cast<int>(gridDim.y - blockIdx.y);
-  if (chunk < 0) return;
+  if (chunk < 0) {
+    leave();
+    return;
+  }
   const int k0 = chunk * ch;
   const int rows = min(ch, kl - k0);
   // columns in use, and the slot of column h's partial among the sequence's chunks
@@ -200,7 +234,6 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     return (static_cast<size_t>(b) * p.Hq * (DIFF ? 2 : 1) + hkv * ncol + h) * p.nsm + chunk;
   };
   const int nblk = (rows + BK - 1) / BK;
-  const int warp = threadIdx.x >> 5;
   const int head_kv = b * p.Hkv + hkv;
   const int* bt = PAGED ? p.block_table + static_cast<size_t>(b) * p.max_blocks : nullptr;
   if constexpr (PAGED) {
@@ -219,37 +252,15 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         p.part_o[ph * D + e % D] = 0.f;
         if (e % D == 0) p.part_lse[ph] = -INFINITY;
       }
+      leave();
       return;
     }
   }
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NSLOT; ++i) {
-      sm100::mbar_init(&kv_full[i], 1);
-      sm100::mbar_init(&kv_empty[i], 1);
-    }
-    sm100::mbar_init(s_full, 1);
-    sm100::mbar_init(p_full, 4);
-    sm100::mbar_init(o_full, 1);
-    sm100::mbar_init(q_ready, 4);
-    sm100::mbar_init(drain, 1);
-    sm100::mbar_init(&mx_bar[0], 4);
-    sm100::mbar_init(&mx_bar[1], 4);
-    sm100::mbar_init(sum_bar, 4);
-    *abort_flag = 0;
-    sm100::fence_barrier_init();
-  }
-  if (!DIFF && warp == 0 && sm100::lane_id() == 0) {
-    sm100::prefetch_tmap(&tmK);
-    sm100::prefetch_tmap(&tmV);
-  }
-  if (warp == 1) {
-    sm100::tmem_alloc(tmem_slot, 32);
-    sm100::tmem_relinquish();
-  }
-  sm100::tc_fence_before();
-  __syncthreads();
-  sm100::tc_fence_after();
+  if constexpr (DIFF)
+    sm100::grid_launch_dependents();  // the combine's set-up: it reads the lengths before its wait
+  else
+    set_up();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS = tmem, tO = tmem + NH;  // S^T: columns 0-15, O^T: 16-31
 
