@@ -149,7 +149,34 @@ constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 // a 128-key block is copied as page segments of min(page, 128) rows (4-D tensor
 // map), and segments past the sequence's last page are addressed at page
 // n_pages, out of range, so the copy fills them with zeros.
-template <int D, bool PAGED, bool DIFF = false>
+// One value per lane and column -> op over the lanes, by halving: in each step a lane trades half of
+// its columns with a partner, so N columns take N + log2(32 / N) shuffles instead of 5 N.
+// Lane i ends with column i / (32 / N).
+// Measured on B200 (one differential decode after another, 5 N shuffles / these / these with
+// eight columns where groups have up to four heads): B4 Hkv8 d128 cache 8192 22.3 / 19.5 / 18.1 us,
+// B16 4096 39 / 36.5 / 35.3, B7 Hkv2 d64 in groups of eight 9001 16.0 / 14.8 / 14.6.
+template <int N, typename Op>
+__device__ __forceinline__ float warp_columns(const float (&v)[N], const Op& op) {
+  float w[N];
+#pragma unroll
+  for (int h = 0; h < N; ++h) w[h] = v[h];
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n >>= 1, o >>= 1) {
+    const bool up = (sm100::lane_id() & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? w[i] : w[i + n];
+      w[i] = op(up ? w[i + n] : w[i], __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+#pragma unroll
+  for (; o >= 1; o >>= 1) w[0] = op(w[0], __shfl_xor_sync(0xffffffffu, w[0], o));
+  return w[0];
+}
+
+// NC: columns that hold a head (differential: a map of one), at most; the others cost nothing.
+template <int D, bool PAGED, bool DIFF = false, int NC = NH>
 __global__ void __launch_bounds__(NTHREADS, 2)
     split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const SplitParams p) {
@@ -382,9 +409,9 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     __syncwarp();
     if (sm100::lane_id() == 0) sm100::mbar_arrive(q_ready);
 
-    float m_use[NH], l[NH];
+    float m_use[NC], l[NC];
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
+    for (int h = 0; h < NC; ++h) {
       m_use[h] = -INFINITY;
       l[h] = 0.f;
     }
@@ -400,36 +427,41 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       sm100::tmem_ld16(tS + lane_base, s);
       sm100::tmem_ld_wait();
       const bool valid = j * BK + r < rows;
-      float v[NH];
+      float v[NC];
 #pragma unroll
-      for (int h = 0; h < NH; ++h)
+      for (int h = 0; h < NC; ++h)
         v[h] = (valid && h < ncol) ? __uint_as_float(s[h]) * p.scale_log2 : -INFINITY;
       // block maxima per head: within the warp, then across the four warps
       // (through shared memory and an mbarrier, so that every wait is bounded;
       // two buffers: a warp writes block j + 2's maxima only after all four
       // warps arrived for block j + 1, i.e. after they read block j's)
       float* rw = red + (j & 1) * 4 * NH;
+      if constexpr (DIFF) {
+        const float m = warp_columns(v, [](float x, float y) { return fmaxf(x, y); });
+        if (sm100::lane_id() % (32 / NC) == 0) rw[q * NH + sm100::lane_id() / (32 / NC)] = m;
+      } else {
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        float m = v[h];
+        for (int h = 0; h < NC; ++h) {
+          float m = v[h];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (sm100::lane_id() == h) rw[q * NH + h] = m;
+          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (sm100::lane_id() == h) rw[q * NH + h] = m;
+        }
       }
       __syncwarp();
       if (sm100::lane_id() == 0) sm100::mbar_arrive(&mx_bar[j & 1]);
       if (!(ok = sm100::mbar_wait(&mx_bar[j & 1], (j >> 1) & 1, abort_flag, p.status, 28))) break;
       bool need = false;
-      float mb[NH];
+      float mb[NC];
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
+      for (int h = 0; h < NC; ++h) {
         mb[h] = fmaxf(fmaxf(rw[h], rw[NH + h]), fmaxf(rw[2 * NH + h], rw[3 * NH + h]));
         need |= mb[h] > m_use[h] + RESCALE_THRESHOLD;
       }
       if (need) {  // uniform: every thread saw the same maxima
-        float alpha[NH];
+        float alpha[NC];
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
+        for (int h = 0; h < NC; ++h) {
           const float mn = fmaxf(m_use[h], mb[h]);
           alpha[h] = (m_use[h] == -INFINITY) ? 0.f : sm100::ex2(m_use[h] - mn);
           m_use[h] = mn;
@@ -442,13 +474,13 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           sm100::tmem_ld16(tO + lane_base, o);
           sm100::tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < NH; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
+          for (int h = 0; h < NC; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
           sm100::tmem_st16(tO + lane_base, o);
           sm100::tmem_st_wait();
         }
       }
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
+      for (int h = 0; h < NC; ++h) {
         if (h < ncol) {
           const float pv = (v[h] == -INFINITY) ? 0.f : sm100::ex2(v[h] - m_use[h]);
           l[h] += pv;
@@ -480,12 +512,17 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     // ---- partial of the chunk: l over the 128 key rows, O^T row d = r
     if (ok) ok = sm100::mbar_wait(o_full, 0, abort_flag, p.status, 27);
     float* rs = red + 2 * 4 * NH;
+    if constexpr (DIFF) {
+      const float x = warp_columns(l, [](float a, float b) { return a + b; });
+      if (sm100::lane_id() % (32 / NC) == 0) rs[q * NH + sm100::lane_id() / (32 / NC)] = x;
+    } else {
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      float x = l[h];
+      for (int h = 0; h < NC; ++h) {
+        float x = l[h];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (sm100::lane_id() == h) rs[q * NH + h] = x;
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (sm100::lane_id() == h) rs[q * NH + h] = x;
+      }
     }
     __syncwarp();
     if (sm100::lane_id() == 0) sm100::mbar_arrive(sum_bar);
@@ -498,7 +535,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     }
     const bool live = ok && !*abort_flag;
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
+    for (int h = 0; h < NC; ++h) {
       if (h >= ncol) break;
       const float ls = rs[h] + rs[NH + h] + rs[2 * NH + h] + rs[3 * NH + h];
       const size_t ph = part_slot(h);
@@ -672,7 +709,7 @@ __global__ void __launch_bounds__(32 * DC_WARPS) diff_combine_kernel(const DiffC
 // (B64 Hq32 Hkv8 d128, cache 32768, k_len ~ U[1024, 32768], 64-row pages in a
 // random order): the paged cache reads at 6951 GB/s, the same rate as the
 // contiguous cache (the earlier CUDA-core split kernel: 6066-6171 GB/s).
-template <int D, bool PAGED, bool DIFF = false>
+template <int D, bool PAGED, bool DIFF = false, int NC = tc::NH>
 cudaError_t launch_split(const SplitParams& sp, cudaStream_t s) {
   CUtensorMap tk, tv;
   const long long heads = static_cast<long long>(sp.B) * sp.Hkv;
@@ -684,7 +721,7 @@ cudaError_t launch_split(const SplitParams& sp, cudaStream_t s) {
             : attn_bwd_impl::make_tmap_rows(&tk, sp.K, D, sp.Lmax, heads, tc::BK) &&
                   attn_bwd_impl::make_tmap_rows(&tv, sp.V, D, sp.Lmax, heads, tc::BK);
   if (!maps) return attn_host::report(cudaErrorInvalidValue, "decode tensor maps");
-  auto kernel = tc::split_kernel<D, PAGED, DIFF>;
+  auto kernel = tc::split_kernel<D, PAGED, DIFF, NC>;
   cudaError_t e = attn_host::report(attn_host::set_smem(kernel, tc::SMEM_BYTES),
                                     "decode tensor-core kernel shared-memory attribute");
   if (e != cudaSuccess) return e;
@@ -763,8 +800,12 @@ inline cudaError_t launch(const __nv_bfloat16* Q, const __nv_bfloat16* K, const 
 template <int D>
 cudaError_t launch_diff_d(const SplitParams& sp, const DiffCombineParams& cp, bool paged,
                           cudaStream_t s) {
+  // groups of up to four heads have eight columns at most
   const cudaError_t e =
-      paged ? launch_split<D, true, true>(sp, s) : launch_split<D, false, true>(sp, s);
+      2 * sp.G <= 8 ? (paged ? launch_split<D, true, true, 8>(sp, s)
+                             : launch_split<D, false, true, 8>(sp, s))
+                    : (paged ? launch_split<D, true, true>(sp, s)
+                             : launch_split<D, false, true>(sp, s));
   if (e != cudaSuccess) return e;
   return attn_host::report(
       attn_host::launch_overlapped(diff_combine_kernel<D>, dim3(sp.B * sp.Hq), dim3(32 * DC_WARPS),
