@@ -137,7 +137,8 @@ constexpr int HPANEL = NH * 128;    // 2 KB: a 16-row x 64-column panel
 constexpr int OFF_RING = 0;
 constexpr int OFF_Q = NSLOT * SLOT;            // Q tile, 2 panels
 constexpr int OFF_P = OFF_Q + 2 * HPANEL;      // P tile, 2 panels
-constexpr int OFF_RED = OFF_P + 2 * HPANEL;    // [2][4 warps][NH] block maxima, [4][NH] sums
+constexpr int OFF_P2 = OFF_P + 2 * HPANEL;     // a second one (differential)
+constexpr int OFF_RED = OFF_P2 + 2 * HPANEL;   // [2][4 warps][NH] block maxima, [4][NH] sums
 constexpr int OFF_BAR = OFF_RED + 3 * 4 * NH * 4;
 constexpr int SMEM_BYTES = OFF_BAR + 256 + 1024;  // barriers + alignment slack
 constexpr int NTHREADS = 6 * 32;
@@ -199,7 +200,17 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   uint64_t* drain = s_full + 4;
   uint64_t* mx_bar = s_full + 5;   // [2]: the softmax warps' block maxima are in
   uint64_t* sum_bar = s_full + 7;  // the softmax warps' row sums are in
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 8);
+  // differential: the next block's scores form beside this block's softmax, in a second
+  // buffer, and there are two of P as well (one decode after another, d128 Hkv8: B4 cache 8192
+  // 18.2 -> 16.6 us, B8 2048 13.7 -> 12.8, B16 4096 35.7 both)
+  uint64_t* s_full1 = s_full + 8;  // of odd blocks
+  uint64_t* pv_done = s_full + 9;
+  constexpr uint32_t TCOLS = DIFF ? 64 : 32;
+  auto s_bar = [&](int j) { return DIFF && (j & 1) ? s_full1 : s_full; };
+  auto s_par = [&](int j) { return static_cast<uint32_t>(DIFF ? (j >> 1) & 1 : j & 1); };
+  auto s_at = [&](int j) { return DIFF ? NH * static_cast<uint32_t>(j & 1) : 0u; };
+  auto p_at = [&](int j) { return DIFF && (j & 1) ? OFF_P2 : OFF_P; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 10);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* red = reinterpret_cast<float*>(smem + OFF_RED);
 
@@ -218,6 +229,10 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       sm100::mbar_init(&mx_bar[0], 4);
       sm100::mbar_init(&mx_bar[1], 4);
       sm100::mbar_init(sum_bar, 4);
+      if constexpr (DIFF) {
+        sm100::mbar_init(s_full1, 1);
+        sm100::mbar_init(pv_done, 1);
+      }
       *abort_flag = 0;
       sm100::fence_barrier_init();
     }
@@ -226,7 +241,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       sm100::prefetch_tmap(&tmV);
     }
     if (warp == 1) {
-      sm100::tmem_alloc(tmem_slot, 32);
+      sm100::tmem_alloc(tmem_slot, TCOLS);
       sm100::tmem_relinquish();
     }
     sm100::tc_fence_before();
@@ -241,7 +256,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     sm100::grid_wait();
   }
   auto leave = [&]() {  // a block without work
-    if (DIFF && warp == 1) sm100::tmem_dealloc(*tmem_slot, 32);
+    if (DIFF && warp == 1) sm100::tmem_dealloc(*tmem_slot, TCOLS);
   };
   // grid (sequence x kv head, chunk position counted from the sequence's end)
   const int hkv = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
@@ -289,7 +304,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   else
     set_up();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tO = tmem + NH;  // S^T: columns 0-15, O^T: 16-31
+  const uint32_t tS = tmem, tO = tmem + (DIFF ? 2 : 1) * NH;  // S^T: columns 0-15 (two), O^T: the next
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -333,30 +348,53 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       __syncwarp();
     };
     const uint64_t qd = sm100::sdesc_sw128(sbase + OFF_Q, 16, 1024);
-    const uint64_t pd = sm100::sdesc_sw128(sbase + OFF_P, 16, 1024);
     bool ok = sm100::mbar_wait(q_ready, 0, abort_flag, p.status, 22);
-    for (int j = 0; j < nblk && ok; ++j) {
-      const int uk = 2 * j, uv = 2 * j + 1;
-      const int ks = uk % NSLOT, vs = uv % NSLOT;
-      if (!(ok = sm100::mbar_wait(&kv_full[ks], (uk / NSLOT) & 1, abort_flag, p.status, 23))) break;
+    // S^T = K Q^T: both K-major; K steps of 16 d (32 bytes) inside a panel
+    auto scores = [&](int j) -> bool {
+      const int uk = 2 * j, ks = uk % NSLOT;
+      if (!sm100::mbar_wait(&kv_full[ks], (uk / NSLOT) & 1, abort_flag, p.status, 23)) return false;
       sm100::tc_fence_after();
       if (leader) {
-        // S^T = K Q^T: both K-major; K steps of 16 d (32 bytes) inside a panel
         const uint64_t kd = sm100::sdesc_sw128(sbase + OFF_RING + ks * SLOT, 16, 1024);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          sm100::mma_ss(tS, kd + static_cast<uint64_t>(((k >> 2) * PANEL + (k & 3) * 32) >> 4),
+          sm100::mma_ss(tS + s_at(j), kd + static_cast<uint64_t>(((k >> 2) * PANEL + (k & 3) * 32) >> 4),
                         qd + static_cast<uint64_t>(((k >> 2) * HPANEL + (k & 3) * 32) >> 4),
                         IDESC_S, k > 0 ? 1u : 0u);
       }
-      commit(s_full);
+      commit(s_bar(j));
       commit(&kv_empty[ks]);
+      return true;
+    };
+    auto ready = [&](uint64_t* bar, uint32_t parity) {  // the same answer in every lane
+      const bool r = sm100::mbar_test_wait(sm100::smem_u32(bar), parity);
+      return __shfl_sync(0xffffffffu, static_cast<int>(r), 0) != 0;
+    };
+    if (DIFF && ok) ok = scores(0);
+    for (int j = 0; j < nblk && ok; ++j) {
+      const int uv = 2 * j + 1, vs = uv % NSLOT;
+      bool next = DIFF && j + 1 < nblk;  // the next block's scores are still to be formed
+      if constexpr (DIFF) {
+        // They go first if their K is there before this block's P, into the buffer that the
+        // softmax of block j - 1 has read; else they must not hold this block's V up.
+        // (A bounded number of looks; the waits after them have their own bound.)
+        const int uk = 2 * j + 2;
+        for (uint32_t look = 0; next && look < (1u << 24) && !ready(p_full, j & 1); ++look) {
+          if (!ready(&kv_full[uk % NSLOT], (uk / NSLOT) & 1)) continue;
+          if (!(ok = scores(j + 1))) break;
+          next = false;
+        }
+        if (!ok) break;
+      } else {
+        if (!(ok = scores(j))) break;
+      }
       if (!(ok = sm100::mbar_wait(p_full, j & 1, abort_flag, p.status, 24))) break;
       if (!(ok = sm100::mbar_wait(&kv_full[vs], (uv / NSLOT) & 1, abort_flag, p.status, 25))) break;
       sm100::tc_fence_after();
       if (leader) {
         // O^T += V^T P^T: A = the V tile read MN-major (64-wide d panels 16 KB
         // apart, 8-key groups 1 KB apart), B = P K-major; K steps of 16 keys
+        const uint64_t pd = sm100::sdesc_sw128(sbase + p_at(j), 16, 1024);
         const uint64_t vd = sm100::sdesc_sw128(sbase + OFF_RING + vs * SLOT, PANEL, 1024);
 #pragma unroll
         for (int k = 0; k < BK / 16; ++k)
@@ -365,6 +403,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
                         IDESC_PV, (j > 0 || k > 0) ? 1u : 0u);
       }
       commit(&kv_empty[vs]);
+      if constexpr (DIFF) commit(pv_done);
+      if (next && !(ok = scores(j + 1))) break;
     }
     commit(o_full);
     // every issued MMA must complete before the tensor memory is released
@@ -397,8 +437,9 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     for (int e = t; e < NH * 16; e += 128) {
       const int g = e >> 4, c16 = e & 15;
       if (g >= ncol)
-        *reinterpret_cast<uint4*>(smem + OFF_P + (c16 >> 3) * HPANEL + g * 128 + ((c16 & 7) << 4)) =
-            make_uint4(0u, 0u, 0u, 0u);
+        for (int b2 = 0; b2 < (DIFF ? 2 : 1); ++b2)
+          *reinterpret_cast<uint4*>(smem + p_at(b2) + (c16 >> 3) * HPANEL + g * 128 +
+                                    ((c16 & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
     }
     if constexpr (DP == 1) {  // the second panel of every ring slot: zeros
       for (int e = t; e < NSLOT * (PANEL / 16); e += 128)
@@ -417,14 +458,15 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     }
     // this thread's P entries: row h, key r -> panel r / 64, 16-byte chunk
     // (r % 64) / 8 swizzled by the row, element r % 8
-    uint8_t* p_col = smem + OFF_P + (r >> 6) * HPANEL + ((r & 7) << 1);
+    uint8_t* p_col0 = smem + (r >> 6) * HPANEL + ((r & 7) << 1);
     const int p_chunk = (r & 63) >> 3;
     bool ok = true;
     for (int j = 0; j < nblk && ok; ++j) {
-      if (!(ok = sm100::mbar_wait(s_full, j & 1, abort_flag, p.status, 26))) break;
+      if (!(ok = sm100::mbar_wait(s_bar(j), s_par(j), abort_flag, p.status, 26))) break;
+      uint8_t* p_col = p_col0 + p_at(j);
       sm100::tc_fence_after();
       uint32_t s[NH];
-      sm100::tmem_ld16(tS + lane_base, s);
+      sm100::tmem_ld16(tS + s_at(j) + lane_base, s);
       sm100::tmem_ld_wait();
       const bool valid = j * BK + r < rows;
       float v[NC];
@@ -469,7 +511,11 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         }
         if (j > 0) {
           // O^T holds PV of the previous blocks (complete: this block's S^T was
-          // issued after them); rescale this thread's row (one d index)
+          // issued after them, or, differential, waited for); rescale this thread's row (one d index)
+          if constexpr (DIFF) {
+            if (!(ok = sm100::mbar_wait(pv_done, (j - 1) & 1, abort_flag, p.status, 31))) break;
+            sm100::tc_fence_after();
+          }
           uint32_t o[NH];
           sm100::tmem_ld16(tO + lane_base, o);
           sm100::tmem_ld_wait();
@@ -549,7 +595,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   __syncthreads();
   if (warp == 1) {
     sm100::tc_fence_after();
-    sm100::tmem_dealloc(tmem, 32);
+    sm100::tmem_dealloc(tmem, TCOLS);
   }
 }
 
