@@ -111,7 +111,7 @@ __device__ __forceinline__ int valid_klen(const int* k_lens, int b, int Lmax, in
 // 2g with [q1 0] and 2g + 1 with [0 q2] as their Q rows, so the same two MMAs
 // give both maps' scores and both O^T over one read of K and V; the combine
 // subtracts.  Measured on B200 (B64 Hq32 Hkv8 d128, k_len ~ U[1024, 32768],
-// 64-row pages): 614 us, 6.3 TB/s of cache read; the copies are the limit.  Keys past the
+// 64-row pages): 579 us, 6.7 TB/s of cache read; the copies are the limit.  Keys past the
 // sequence's end may hold anything (a page is handed out unwritten): their scores are dropped by
 // selection, and their V rows, which a zero probability would not silence if
 // they held NaN, are cleared in shared memory before the PV product.
@@ -640,8 +640,8 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const CombineParams p
 // of the cache's capacity (the lengths are on the device), since a short grid leaves
 // SMs without a stream of their own, and a longer one only adds set-up and partials.
 // Measured on B200 (splits for 148 / 296 of them at least, us): B1 Hkv1 d128 cache 131072
-// 27.5 / 42.2, B1 Hkv8 32768 30.7 / 35.8, B16 Hkv8 4096 40.7 / 48.4, B7 Hkv2 d64 9001
-// 19.0 / 19.7; a lower limit of 128 instead of 256 keys: B1 Hkv8 512 9.4 / 10.4.
+// 20.5 / 30.4, B1 Hkv8 32768 24.8 / 29.5, B16 Hkv8 4096 35.6 / 42.3, B7 Hkv2 d64 9001
+// 14.0 / 14.1, B4 Hkv8 8192 16.6 / 14.3.
 inline int diff_chunk(int B, int Hkv, int Lmax) {
   const long long want = 148;
   int ch = CH;
