@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(256)
                   float scale, long long conv_blocks, const float* lam_part, __nv_bfloat16* dlam,
                   int B, int Hq, int Hkv, int Lk, int n_lam, int n_split, const float* kv_part,
                   __nv_bfloat16* dK, __nv_bfloat16* dV) {
-  sm100::grid_launch_dependents();
+  // (no launch of the kernel behind from here: a next backward's preparation, resident early,
+  // cost 1886 -> 1955 us a backward of causal B2 H16 L8192 d128, one after another)
   sm100::grid_wait();
   const int n_kv = (Lk + BN - 1) / BN;
   if (blockIdx.x >= conv_blocks + n_lam) {

@@ -434,10 +434,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   sm100::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if constexpr (MODE == MODE_DIFF) {
-    // the set-up so far ran beside the end of the kernel before; the one behind may set up, too
-    // (not earlier: this block's tensor memory is its own by now)
+    // The set-up so far ran beside the end of the kernel before.  The one behind may set up, too,
+    // where every item has an SM (one after another, B1 H2 L256 d64: 10.9 -> 10.7 us); beside
+    // a call that keeps all SMs it cost more (causal B4 H16 L4096 d128: 453 -> 461).  Not
+    // earlier: this block's tensor memory is its own by now.
     sm100::grid_wait();
-    sm100::grid_launch_dependents();
+    if (p.n_items <= static_cast<int>(gridDim.x)) sm100::grid_launch_dependents();
   }
 
   // consumers' view of the item ring: the k-th item index, or -1 at the end
