@@ -36,7 +36,10 @@
  *   workspace, and the stream.  The library never allocates, frees or
  *   synchronises, except attn_read_device_status (which synchronises `stream`).
  * - Asynchrony: every compute call enqueues kernels on `stream` (a
- *   cudaStream_t; NULL = legacy default stream) and returns at once.
+ *   cudaStream_t; NULL = legacy default stream) and returns at once.  The
+ *   kernels of the differential calls and of the append may be set up while the
+ *   kernel before them on the stream still runs (programmatic dependent launch);
+ *   they touch memory only once it has finished.
  * - Errors: argument errors are detected on the host before anything is
  *   launched and return ATTN_ERR_INVALID or ATTN_ERR_UNSUPPORTED.  A failed
  *   launch returns ATTN_ERR_CUDA.  Errors found on the device (a k_lens entry

@@ -183,3 +183,35 @@ def test_unsound_calls_raise_as_before():
     d96 = torch.zeros(1, 1, 8, 96, dtype=BF, device=dev)
     with pytest.raises(attn.AttnError):
         attn.attn_fwd_diff(d96, d96, d96, lam[:1])
+
+
+@pytest.mark.gpu
+def test_threads_call_at_once():
+    """Four host threads, each on a stream of its own: what one call alone gives."""
+    import threading
+
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)
+    q, k, v = rn(2, 4, 300, 64), rn(2, 2, 300, 64), rn(2, 2, 300, 64)
+    lam, kl = torch.rand(4, generator=g, device="cuda"), torch.tensor([300, 9], dtype=I32, device="cuda")
+    one = q[:, :, :1].contiguous()
+
+    def work():
+        return attn.attn_fwd_diff(q, k, v, lam, causal=True) + \
+            attn.attn_fwd_splitkv_decode_diff(one, k, v, lam, kl)
+
+    want, got = work(), [None] * 4
+    torch.cuda.synchronize()
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got[i] = [work() for _ in range(25)][-1]
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for r in got:
+        assert r is not None and all(torch.equal(a, b) for a, b in zip(r, want))
