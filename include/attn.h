@@ -225,7 +225,9 @@ attn_status_t attn_fwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const at
  * (dK, dV summed over the query heads of a KV head; dlam over the batch and the
  * rows, and over the heads when n_lam = 1).
  *   O, O2, lse as attn_fwd_diff wrote them for the same arguments; dO [B,Hq,Lq,d]
- *   bf16, finite.  dQ [B,Hq,Lq,d], dK, dV [B,Hkv,Lk,d] and dlam [n_lam] are
+ *   bf16, finite.  D_1 and D_2 come from the rounded O and O2, as the plain
+ *   backward's D does: where one key takes all of a row, dP - D_m is that rounding
+ *   instead of zero.  dQ [B,Hq,Lq,d], dK, dV [B,Hkv,Lk,d] and dlam [n_lam] are
  *   written, all bf16, with dK = dV = 0 at and past k_lens[b].  Masks, limits and
  *   errors as attn_fwd_diff.  The workspace holds the fp32 dQ accumulator, four
  *   fp32 statistics per query row, the partial sums of dlam and, where there are

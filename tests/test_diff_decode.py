@@ -79,6 +79,29 @@ def test_decode_matches_definition(B, Hq, Hkv, Lmax, d, lens, page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 8, 4), (128, 4, 4), (128, 32, 4)])
+def test_decode_large_scores_in_long_splits(d, Hq, Hkv):
+    """Scale 1 and enough sequences for splits of many 128-key blocks: the maxima move from block
+    to block, after the next block's scores were formed."""
+    attn = _lib()
+    B, Lmax = 40, 1500
+    lens = [(37 * b * b + 1) % (Lmax + 1) for b in range(B)]
+    Q, K, V, lam = _problem(B, Hq, Hkv, Lmax, d, lens, 13)
+    K *= torch.linspace(0.2, 1.5, Lmax)[:, None].to(BF)  # later keys score higher
+    for b, n in enumerate(lens):
+        K[b, :, n:] = math.nan
+    O, _, lse, tol, _ = ref.fwd(Q, K, V, lam, scale=1.0, k_lens=lens)
+    kl = torch.tensor(lens, dtype=I32, device="cuda")
+    o, l = attn.attn_fwd_splitkv_decode_diff(Q.cuda(), K.cuda(), V.cuda(), lam.cuda(), kl, scale=1.0)
+    ref.assert_within(o, O, tol, "O")
+    ref.assert_lse(l, lse[..., 0])
+    kp, vp, table = _pages(K, V, 64, 3, math.nan)
+    op, lp = attn.attn_fwd_splitkv_decode_diff_paged(Q.cuda(), kp.cuda(), vp.cuda(), table.cuda(),
+                                                     lam.cuda(), kl, scale=1.0)
+    assert torch.equal(op, o) and torch.equal(lp, l)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 def test_decode_large_scores_one_weight_and_infinities_past_the_end(d):
     """Scale 1: the running maxima jump from split to split; garbage is infinite."""
