@@ -782,13 +782,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 64; c += 4) {
-          mx0 = sm100::max3(mx0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          mx1 = sm100::max3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          const float a = __uint_as_float(s[c]), b = __uint_as_float(s[c + 1]);
+          const float e = __uint_as_float(s[c + 2]), f = __uint_as_float(s[c + 3]);
+          mx0 = MODE == MODE_DIFF ? sm100::max3_nan(mx0, a, b) : sm100::max3(mx0, a, b);
+          mx1 = MODE == MODE_DIFF ? sm100::max3_nan(mx1, e, f) : sm100::max3(mx1, e, f);
         }
         // the row max over all 128 keys: exchange with the warp holding the other half
-        red_w[hf * BM + r] = fmaxf(mx0, mx1);
+        if constexpr (MODE == MODE_DIFF) mx0 = sm100::max3_nan(mx0, mx1, mx1);
+        else mx0 = fmaxf(mx0, mx1);
+        red_w[hf * BM + r] = mx0;
         sm100::named_bar_sync(bar_id, 64);
-        const float m_new = fmaxf(fmaxf(mx0, mx1), red_w[(hf ^ 1) * BM + r]) * sl2j;
+        const float mx_o = red_w[(hf ^ 1) * BM + r];
+        const float m_new =
+            (MODE == MODE_DIFF ? sm100::max3_nan(mx0, mx_o, mx_o) : fmaxf(mx0, mx_o)) * sl2j;
         const bool need = m_new > m_use + RESCALE_THRESHOLD;
         if constexpr (C::SEP_P) {
           // O and P_t are written below: PV_t of the previous P must have completed
@@ -818,7 +824,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           m_use = m_upd;
         }
         const float m_sub = (m_use == -INFINITY) ? 0.f : m_use;
-        const float2 negm = make_float2(u_j - m_sub, u_j - m_sub);
+        // Differential heads: a maximum that is NaN, or +inf (whose own exponential is inf - inf),
+        // makes all of the row's exponents NaN: the polynomials alone would turn that score into a
+        // small weight, as they do the masked ones.  (Measured: no difference.)
+        float neg1 = u_j - m_sub;
+        if constexpr (MODE == MODE_DIFF)
+          neg1 = __fmaf_rn(sm100::max3_nan(m_new, 0.f, 0.f), 0.f, -m_sub);
+        const float2 negm = make_float2(neg1, neg1);
         float2 lsum = make_float2(0.f, 0.f);
         auto exp_pair = [&](int cp) -> float2 {
           const float2 x = __ffma2_rn(

@@ -355,6 +355,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// The same, but NaN where an operand is (max drops it).
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // 2^x for a pair of floats on the FMA pipe instead of the special-function
 // unit: Cody-Waite reduction x = n + f with n = round(x) (the 1.5 * 2^23
 // addition rounds to an integer in the low mantissa bits), f in [-1/2, 1/2];
@@ -385,7 +392,7 @@ __device__ __forceinline__ float2 ex2_poly2(float2 x_in) {
 // The same with a degree-4 polynomial (2.79e-6, from exp2_poly_fit.py 4), for sums that are
 // kept as a statistic, and without the zeroing of inputs below -125: those (-inf
 // included) give about 2^-126, so the caller must know a row without any other
-// entry by its maximum.
+// entry by its maximum.  So does NaN: the caller must know that one, too.
 __device__ __forceinline__ float2 ex2_poly4_nz(float2 x) {
   x.x = fmaxf(x.x, -126.f);
   x.y = fmaxf(x.y, -126.f);

@@ -206,8 +206,9 @@ attn_status_t attn_bwd_sliding(const attn_bf16_t* Q, const attn_bf16_t* K, const
  *   O [B,Hq,Lq,d] bf16.  O2 [B,Hq,Lq,d] bf16 (O_2, for the backward; may be
  *   NULL).  lse [B,Hq,2,Lq] fp32 (may be NULL).  d = 64 or 128.  The other
  *   arguments, masks and errors as attn_fwd; a row that sees no key gets O = 0,
- *   O2 = 0 and both lse = -inf.  K and V rows at and past k_lens[b] are not used
- *   and may hold anything.  More than 2^30 128-row tiles over all heads return
+ *   O2 = 0 and both lse = -inf.  A score that is NaN or +inf, at any key that a row
+ *   sees, makes that row's O and that map's O2 and lse NaN.  K and V rows at and past
+ *   k_lens[b] are not used and may hold anything.  More than 2^30 128-row tiles over all heads return
  *   ATTN_ERR_UNSUPPORTED.  A call of at most attn_num_sms() query tiles
  *   (B * Hq * ceil(Lq / 128)) uses no counter of the workspace: it need only be
  *   cleared beforehand if its status word is to be read.
@@ -330,7 +331,10 @@ attn_status_t attn_fwd_splitkv_decode_paged(const attn_bf16_t* Q, const attn_bf1
  *   most 8 (any number); the split length goes by B, Hkv and the cache's
  *   capacity, so the workspace is attn_decode_diff_workspace_size(B, Hq, Hkv,
  *   Lmax, d) bytes (Lmax = max_blocks * page_size for a paged cache).
- * Cache rows at and past k_lens[b] are not used and may hold anything.  The
+ * Cache rows at and past k_lens[b] are not used and may hold anything.  An element
+ * of a visible key that is not finite makes its heads' O NaN, and the lse of the other
+ * map at least (each map's scores are formed over the whole row, with zeros for the
+ * other half).  The
  * workspace need only be cleared beforehand if its status word is to be read.
  */
 size_t attn_decode_diff_workspace_size(int B, int Hq, int Hkv, int Lmax, int d);
