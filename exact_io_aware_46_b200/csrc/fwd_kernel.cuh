@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           break;
         int w = static_cast<int>(blockIdx.x);
         if (MODE == MODE_DIFF && k > 0 && p.n_items <= static_cast<int>(gridDim.x))
-          w = -1;  // an item a CTA: the counters are not used (a small call need not clear them)
+          w = -1;  // an item a CTA: the counters are not used
         else if (k > 0)
           w = atomicAdd(p.sched, 1) + static_cast<int>(gridDim.x);
         if (w >= p.n_items) w = -1;
@@ -1110,7 +1110,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     sm100::tc_fence_after();
     sm100::tmem_dealloc(tmem, 512);
   }
-  if (threadIdx.x == 0) {
+  if (MODE == MODE_DIFF && p.n_items <= static_cast<int>(gridDim.x)) {
+    // no CTA used the counters: zero them, since the memory may never have been cleared and the
+    // next call on it may need them
+    if (blockIdx.x == 0 && threadIdx.x < 2) p.sched[threadIdx.x] = 0;
+  } else if (threadIdx.x == 0) {
     // the last CTA to finish re-arms the dynamic scheduler for the next launch
     __threadfence();
     if (atomicAdd(p.sched + 1, 1) == static_cast<int>(gridDim.x) - 1) {

@@ -210,8 +210,11 @@ attn_status_t attn_bwd_sliding(const attn_bf16_t* Q, const attn_bf16_t* K, const
  *   sees, makes that row's O and that map's O2 and lse NaN.  K and V rows at and past
  *   k_lens[b] are not used and may hold anything.  More than 2^30 128-row tiles over all heads return
  *   ATTN_ERR_UNSUPPORTED.  A call of at most attn_num_sms() query tiles
- *   (B * Hq * ceil(Lq / 128)) uses no counter of the workspace: it need only be
- *   cleared beforehand if its status word is to be read.
+ *   (B * Hq * ceil(Lq / 128), at least one) sets the workspace's counters to zero and
+ *   needs none of them: the workspace need only be cleared beforehand if its status
+ *   word is to be read.  Before a call of more tiles the counters must be zero: from
+ *   attn_clear_device_status, or from an earlier sound call of attn_fwd_diff or (with
+ *   Lq > 0) attn_bwd_diff on the same workspace.
  */
 size_t attn_fwd_diff_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk, int d);
 attn_status_t attn_fwd_diff(const attn_bf16_t* Q, const attn_bf16_t* K, const attn_bf16_t* V,
