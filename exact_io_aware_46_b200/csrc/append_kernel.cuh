@@ -215,12 +215,17 @@ __global__ void __launch_bounds__(NTHREADS) append_kernel(const Params p) {
       row = next;
     }
   }
-  // the offsets as a whole, once: a sequence that breaks the rules may own no token
+  // the offsets as a whole, once, and the lengths of sequences without new tokens: one that
+  // breaks the rules may own no token
   if (p.cu && blockIdx.x == 0 && blockIdx.y == 0) {
     bool bad = threadIdx.x == 0 && __ldg(p.cu) != 0;
     for (int i = threadIdx.x; i < p.B; i += NTHREADS) {
       const int c0 = __ldg(p.cu + i), c1 = __ldg(p.cu + i + 1);
       bad |= c0 < 0 || c1 < c0 || c1 > p.T;
+      if (c0 == c1) {
+        const int kl = __ldg(p.k_lens + i);
+        bad |= kl < 0 || kl > cap;
+      }
     }
     if (bad) atomicOr(p.status, BAD_KLEN);
   }

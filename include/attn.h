@@ -381,9 +381,10 @@ attn_status_t attn_fwd_splitkv_decode_diff_paged(
  *   [n_pos, rope_dim / 2].  rope_dim is a multiple of 16 up to d / maps, or 0 (no
  *   rotation, tables may be NULL); else ATTN_ERR_UNSUPPORTED.  d = 64 or 128.
  *   Device errors: a sequence whose offsets break the rules, whose k_lens entry is
- *   below n_b or above the cache's capacity, or a row past n_pos, sets
+ *   below n_b (n_b = 0 included) or above the cache's capacity, or a row past n_pos, sets
  *   ATTN_DEV_BAD_KLEN; a block-table entry outside [0, n_pages) sets
  *   ATTN_DEV_BAD_PAGE.  The tokens concerned write nothing, Q_out included.
+ *   With T = 0 nothing is launched or checked on the device.
  *   Only the workspace's status word is used; clear it beforehand to read it.
  */
 size_t attn_kv_append_paged_workspace_size(void);
