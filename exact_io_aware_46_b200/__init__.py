@@ -941,6 +941,11 @@ def attn_kv_append_paged(K, V, Kp, Vp, block_table, k_lens, cu_seqlens=None, Q=N
             raise ValueError(f"cos must be [n_pos, rope_dim / 2], got {tuple(cos.shape)}")
         n_pos, rope = int(cos.shape[0]), 2 * int(cos.shape[1])
         _need(sin, "sin", torch.float32, cos.shape, dev)
+    # the library takes these as 32-bit numbers
+    for n, what in ((B, "sequences"), (block_table.shape[1], "blocks a sequence"),
+                    (n_pos, "positions")):
+        if n > 0x7fffffff:
+            raise ValueError(f"{n} {what} are past the limit of 2^31 - 1")
     nbytes = attn_kv_append_paged_workspace_size()
     if workspace is not None:
         _ws_check(workspace, nbytes, dev)
