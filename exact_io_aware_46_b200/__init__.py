@@ -36,16 +36,43 @@ import functools
 import math
 import os
 import threading
+import warnings
 
 import torch
 
-try:  # checks and marshalling of the differential calls' common form, compiled
-    from . import _binding
-except ImportError:  # not built: the same in Python
-    _binding = None
-
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libattn.so")
+
+#: what the compiled binding was built against: it uses torch's C++ classes, whose layout may
+#: change without any symbol missing
+BINDING_TAG = (f"exact_io_aware_46_b200 binding for torch {torch.__version__}, "
+               f"C++11 ABI {int(torch.compiled_with_cxx11_abi())}")
+
+
+def _load_binding(load):
+    """The compiled checks and marshalling of the differential calls' common form; None, with a
+    warning if the library itself is built, where it is missing or was built for another torch
+    (the same then runs in Python)."""
+    try:
+        module = load()
+        if getattr(module, "BUILT_FOR", None) == BINDING_TAG:
+            return module
+        why = f"it was built for {getattr(module, 'BUILT_FOR', 'something else')}"
+    except ImportError as e:
+        why = str(e)
+    if os.path.exists(LIB_PATH):
+        warnings.warn(f"the compiled binding is not used, small calls cost more on the host: {why}; "
+                      "run `python -m exact_io_aware_46_b200.build`", RuntimeWarning, stacklevel=3)
+    return None
+
+
+def _import_binding():
+    from . import _binding
+
+    return _binding
+
+
+_binding = _load_binding(_import_binding)
 
 (ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_TIMEOUT,
  ATTN_ERR_CAPACITY) = range(6)

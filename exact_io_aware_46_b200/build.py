@@ -1,5 +1,6 @@
 """Builds the CUDA library ``libattn.so`` (nvcc, sm_100a only) and the Python extension
-``_binding`` (g++, against torch's headers) in-tree."""
+``_binding`` (g++, against torch's headers) in-tree.  The library works without the extension, so
+a failure to build that one is a warning."""
 
 from __future__ import annotations
 
@@ -8,6 +9,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -37,10 +39,21 @@ def up_to_date(so: str, srcs) -> bool:
     return all(os.path.getmtime(s) <= t for s in srcs)
 
 
+def binding_up_to_date() -> bool:
+    from . import BINDING_TAG
+
+    if not up_to_date(BINDING, [SRC_BINDING, os.path.join(ROOT, "include", "attn.h")]):
+        return False
+    with open(BINDING, "rb") as f:  # the tag is a string of the extension
+        return BINDING_TAG.encode() in f.read()
+
+
 def build_binding(force: bool = False) -> str:
-    if not force and up_to_date(BINDING, [SRC_BINDING, os.path.join(ROOT, "include", "attn.h")]):
+    if not force and binding_up_to_date():
         return BINDING
     import torch
+
+    from . import BINDING_TAG
 
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
@@ -50,15 +63,15 @@ def build_binding(force: bool = False) -> str:
     tmp = BINDING + f".tmp{os.getpid()}"
     subprocess.check_call(
         [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+         f'-DBINDING_TAG="{BINDING_TAG}"']
         + ["-I" + i for i in inc] + [SRC_BINDING, "-o", tmp, "-L" + os.path.join(t, "lib")]
         + ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"])
     os.replace(tmp, BINDING)
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_binding(force)
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date(SO, sources()):
         return SO
     tmp = SO + f".tmp{os.getpid()}"
@@ -68,6 +81,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.check_call(cmd)
     os.replace(tmp, SO)
     return SO
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    so = build_library(force, verbose)
+    try:
+        build_binding(force)
+    except (OSError, subprocess.CalledProcessError) as e:
+        if os.path.exists(BINDING):  # of other sources or another torch
+            os.remove(BINDING)
+        warnings.warn(f"the Python extension was not built, its calls run in Python: {e}",
+                      RuntimeWarning, stacklevel=2)
+    return so
 
 
 if __name__ == "__main__":

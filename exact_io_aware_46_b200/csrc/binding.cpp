@@ -408,4 +408,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  // what it was compiled against, compared when it is loaded
+  if (m && PyModule_AddStringConstant(m, "BUILT_FOR", BINDING_TAG) < 0) Py_CLEAR(m);
+  return m;
+}
