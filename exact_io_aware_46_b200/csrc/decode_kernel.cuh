@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   }
 
   if constexpr (DIFF)
-    sm100::grid_launch_dependents();  // the combine's set-up: it reads the lengths before its wait
+    sm100::grid_launch_dependents();  // the combine's set-up
   else
     set_up();
   const uint32_t tmem = *tmem_slot;
@@ -672,8 +672,9 @@ struct DiffCombineParams {
 // Joins both maps' partials (the normalised rule of decode_combine_kernel, per
 // map) and subtracts: O = O_1 - lam O_2.  One block per (sequence, query head), even
 // warps for the first map and odd ones for the second, four splits of a map at a time,
-// each lane D / 32 columns.  The length, the log-sum-exps and the first partials are
-// requested together: a row past the length is dropped by selection.
+// each lane D / 32 columns.  The weight, the length, the log-sum-exps and the first
+// partials are requested together: a row past the length is dropped by selection.  All of
+// it behind the wait (reading the weight and the length before it measured the same).
 constexpr int DC_WARPS = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * DC_WARPS) diff_combine_kernel(const DiffCombineParams p) {
@@ -686,9 +687,9 @@ __global__ void __launch_bounds__(32 * DC_WARPS) diff_combine_kernel(const DiffC
   const int m = warp & 1;
   const float* lp = p.part_lse + (static_cast<size_t>(bh) * 2 + m) * p.nsm;
   const float* op = p.part_o + (static_cast<size_t>(bh) * 2 + m) * p.nsm * D + lane * EPL;
+  sm100::grid_wait();
   const float lam = __ldg(p.lam + (p.n_lam == 1 ? 0 : h));
   int kl = __ldg(p.k_lens + b);
-  sm100::grid_wait();
   if (kl < 0 || kl > p.Lmax) kl = 0;  // reported by the split kernel
   const int n = (kl + p.ch - 1) / p.ch;
   auto load = [&](int c, float (&v)[EPL]) {
