@@ -277,7 +277,7 @@ __device__ __forceinline__ constexpr bool poly_pair(int cp) {
 // 442, a quarter 434, three eighths 455; every fourth pair 422 against two of eight 426, after
 // the product with V was put in two parts), by the degree-4 polynomial without the
 // zeroing of masked entries, which costs less than the zeroing saved (440 us with the
-// degree-3 form above) and keeps the log-sum-exp to 1e-6.
+// degree-3 form above) and adds at most 2.9e-6 to the log-sum-exp.
 __device__ __forceinline__ constexpr bool diff_poly_pair(int cp) { return (cp & 3) == 3; }
 
 // S_t = Q_t K_j^T: 128 x 128 (keys) x D, both operands K-major SW128 panels.
