@@ -925,7 +925,8 @@ def attn_kv_append_paged(K, V, Kp, Vp, block_table, k_lens, cu_seqlens=None, Q=N
     gives each sequence's new tokens (None: one token per sequence).  cos/sin fp32
     [n_pos, rope_dim/2] or both None (no rotation); maps = 2 rotates each half of a
     differential head by itself.  Returns the rotated Q [T,Hq,d] (None without Q); rows behind
-    the last sequence are left as they were."""
+    the last sequence are left as they were.  For attn_fwd_splitkv_decode_paged allocate the pages
+    zeroed: it wants finite values behind a sequence's end (the differential decode does not)."""
     if stream is None and _binding is not None:
         done = _binding.append(K, V, Kp, Vp, block_table, k_lens, cu_seqlens, Q, Q_out, cos, sin,
                                maps, interleaved, workspace)
