@@ -153,7 +153,8 @@ constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 // One value per lane and column -> op over the lanes, by halving: in each step a lane trades half of
 // its columns with a partner, so N columns take N + log2(32 / N) shuffles instead of 5 N.
 // Lane i ends with column i / (32 / N).
-// Measured on B200 (one differential decode after another, 5 N shuffles / these / these with
+// Measured on B200 (one differential decode after another in a graph, caches held in L2, lengths
+// of 100 to 8000, 2000 to 3500 and 1 to 9001 rows; 5 N shuffles / these / these with
 // eight columns where groups have up to four heads): B4 Hkv8 d128 cache 8192 22.3 / 19.5 / 18.1 us,
 // B16 4096 39 / 36.5 / 35.3, B7 Hkv2 d64 in groups of eight 9001 16.0 / 14.8 / 14.6.
 template <int N, typename Op>
@@ -639,11 +640,15 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const CombineParams p
 // Keys per split: the longest of 2048, 1024, ..., 128 that still gives every SM a split
 // of the cache's capacity (the lengths are on the device), since a short grid leaves
 // SMs without a stream of their own, and a longer one only adds set-up and partials.
-// Measured on B200 (splits for 148 / 296 of them at least, us): B1 Hkv1 d128 cache 131072
-// 20.5 / 30.4, B1 Hkv8 32768 24.8 / 29.5, B16 Hkv8 4096 35.6 / 42.3, B7 Hkv2 d64 9001
-// 14.0 / 14.1, B4 Hkv8 8192 16.6 / 14.3.
+// Measured on B200 (splits for 148 / 296 of them at least, us a decode, one after another, groups of
+// four heads, of eight at d64, every sequence as long as the cache; the same cache again and
+// again, and caches in turn, 700 MB in all, that L2 does not hold): B1 Hkv1 d128 cache 131072
+// 17.6 / 28.6 and 22.0 / 30.8, B1 Hkv8 32768 27.0 / 32.3 and 27.1 / 33.0, B16 Hkv8 4096
+// 48.4 / 50.3 and 48.5 / 50.2, B7 Hkv2 d64 9001 15.5 / 21.0 and 16.2 / 22.0, B4 Hkv8 8192
+// 27.5 / 31.4 both ways.  (Shorter sequences leave splits empty: four of 8000, 100, 5000 and 3000
+// keys in caches of 8192 rows, held in L2, took 16.6 / 14.3.)
 inline int diff_chunk(int B, int Hkv, int Lmax) {
-  const long long want = 148;
+  const long long want = 148;  // the SMs of every B200; the workspace query takes no device
   int ch = CH;
   while (ch > 128 && static_cast<long long>(B) * Hkv * ((Lmax + ch - 1LL) / ch) < want) ch /= 2;
   return ch;

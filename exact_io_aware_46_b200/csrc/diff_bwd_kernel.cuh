@@ -23,15 +23,16 @@
 //   dQ_m^T = K_m^T dS_m^T      (SS, M = 64, lanes = head dimension, over the dP columns:
 //                               map 1 in lanes 0-15 of each 32, map 2 in lanes 16-31)
 // dV (d columns) and dK (64 per map) stay in TMEM for the item: 512 columns in all.
-// At d = 64 the maps are 32 columns wide but the products still run over the whole
-// 64-column panel -- with N this small an SS product is bound by reading A, and M has
-// no smaller value -- and the half that belongs to the other map is not read.
+// At d = 64 the maps are 32 columns wide but the dK and dQ products still run over the whole
+// 64-column panel, and the half that belongs to the other map is not read: 14 d FLOP are
+// executed where 10 d are needed.  dQ's M has no smaller value; dK at N = 32 is not tried.
 //
 // Warps 0-7 and 8-15 work half 0 and half 1, half a tile apart: one group's scalar
 // work (a key row per thread, two warps per row) runs while the tensor core works
 // for the other.  Per half and tile a group forms P_1, adds the tile before's dQ^T
 // into the fp32 accumulator, and then forms P_2, W and both dS sixteen columns at a
-// time, dP at hand, so that 96 registers hold it all.  dQ^T goes out by 4-byte reductions
+// time, dP at hand, so that 96 registers hold nearly all of it (ptxas: 72 bytes of spill stores
+// and 164 of loads a thread at d = 128, 60 and 176 at d = 64).  dQ^T goes out by 4-byte reductions
 // that cover 128 contiguous bytes (the accumulator's columns are ordered as the lanes
 // are).  Those additions happen at L2, at a rate that no way of sending them changed
 // (64 KB per tile and SM in 2.1 us: reductions of 4 bytes a lane 4628 GB/s, bulk
@@ -39,19 +40,23 @@
 // so the way that needs no shared memory was taken.  Warp 16 feeds K, V and Q by TMA,
 // warps 18 and 19 a half's statistics and dO each, warp 17 issues the MMAs.
 //
-// Measured on B200 (causal B2 H16 L8192 d128): dQ staged in the dS buffers and one tile
+// Measured on B200 (causal B2 H16 L8192 d128, calls timed alone; one after another the kernel
+// draws the card's power limit and takes a sixth longer): dQ staged in the dS buffers and one tile
 // at a time 2715 us; dQ by reductions 2392; halves in turn 2031; fewer waits and no
 // divisions 1869; P_2 and dS in one go 1672; dK_1 by TS 1637; set-up overlapped with the
 // kernel before 1601; P_1 kept as scaled fp16 1638 (for its precision).  What bounds it now is
-// shared memory: the products read 416 KB of operands per 128-row tile (an SS product at
-// N = 64 is fed at ~95 of the 128 bytes a cycle), the copies in, the dS and the statistics'
-// broadcasts take another 190 KB, about 4700 of the ~6300 cycles of a tile.
+// not established.  A 128-row tile takes ~6300 cycles.  Its products read 416 KB of operands from
+// shared memory and copies, dS and statistics' broadcasts pass another 190 KB, ~4850 cycles at
+// 128 bytes a cycle; but with a third of those cycles' worth of statistics' reads left out (timing
+// only) it ran 1.6 % faster, so that is not the limit alone.  The tensor pipe is 51 % active and
+// 68 % busy on its issue side, the special-function unit 35 %, issue 43 %.
 //
 // dlam needs more of P_2 than bf16 gives: its terms P_2 dP have both signs, and
 // the roundings of P_2 (2^-9 relative on average) do not shrink with the sum.
 // The sums take P_2 in fp32, as it comes from the exponential.  Sums per (item, head,
-// warp) go to the workspace and are added in a fixed order, so dlam is the same
-// from run to run.
+// warp) go to the workspace and are added in a fixed order, in fp64, so dlam is the same
+// from run to run.  It is rounded once, to bf16 like every gradient of this library (2^-8 of
+// the sum at most): callers that accumulate over several calls add in a type of their own.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -699,7 +704,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   } else {
     // ------------------------------------------------------------ P, W and dS; dQ
     // Little state is kept across tiles (barriers as 32-bit addresses, one accumulator
-    // pointer, the mask as one bound): 96 registers hold 48 of probabilities.
+    // pointer, the mask as one bound), since 96 registers have to hold 48 of probabilities.
     const int qd = warp & 3, cq = warp >> 2, lane = sm100::lane_id();
     const int h = cq >> 1;  // half tile of this warp's group
     const int kl_ = qd * 32 + lane;  // key row within the tile = TMEM lane
@@ -959,11 +964,14 @@ struct Args : attn_bwd_impl::Args {
 // the causal mask's unequal items, leave SMs idle behind the longest one.  In units of a
 // tile, a part costs about one more (its K, V, first products and sums); the makespan
 // is the larger of the mean load and the longest part, and the least estimate wins.
-// Measured on B200 (1 part / this rule's parts, us): causal B1 Hq32 Hkv1 L4096 d128 3181 / 454,
-// causal B1 Hq16 Hkv2 L8192 d128 1634 / 875, B1 Hq8 Hkv2 L2048 d128 212 / 72, B1 H4 L2048
-// d128 63 / 42, causal B3 Hq16 Hkv4 L1999 d64 197 / 192 (4 parts would be 185).
+// The lengths are on the device, so a padded batch counts its empty tiles, too.
+// Measured on B200 (1 part / 4 parts / this rule's parts, us a call, one after another): causal B1
+// Hq32 Hkv1 L4096 d128 3212 / 870 / 470, causal B1 Hq16 Hkv2 L8192 d128 1656 / 923 / 988, B1 Hq8
+// Hkv2 L2048 d128 215 / 84 / 81, B1 H4 L2048 d128 64 / 64 / 50, causal B3 Hq16 Hkv4 L1999 d64
+// 197 / 207 / 218, and padded to 1999, 1600 and 1200 keys 197 / 201 / 202: there the rule splits
+// where one part is as good or better.
 inline int n_split(int B, int Hq, int Hkv, int Lq, int Lk, bool causal) {
-  constexpr double SMS = 148.;
+  constexpr double SMS = 148.;  // of every B200; the workspace query takes no device
   const double items = static_cast<double>(B) * Hkv * ((Lk + BN - 1) / BN);
   const double longest = static_cast<double>(Hq / Hkv) * ((Lq + BMQ - 1) / BMQ);
   if (items <= 0. || longest <= 0.) return 1;

@@ -150,7 +150,10 @@ struct Item {
 // row sums are known: the four warps of a lane quarter then each combine a
 // quarter of the columns, o_1 / l_1 - lam o_2 / l_2.  6 d FLOP and two
 // exponentials per visible pair (the single sum (P_1 - lam P_2) V would need 4 d,
-// but its weights only exist once both row sums do).  K and V rows past k_len
+// but its weights only exist once both row sums do).  Its times below are of calls timed alone
+// unless they say "one after another": those draw the card's power limit (causal B4 H16 L4096
+// d128: 498 us at a median of 1642 MHz).  ptxas: 28 bytes of spill stores and 44 of loads a thread
+// at d = 128, 36 and 68 at d = 64.  K and V rows past k_len
 // may hold anything: scores are masked by selection, and V rows are cleared in
 // shared memory before the tile's PV.
 enum : int {
@@ -436,7 +439,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if constexpr (MODE == MODE_DIFF) {
     // The set-up so far ran beside the end of the kernel before.  The one behind may set up, too,
     // where every item has an SM (one after another, B1 H2 L256 d64: 10.9 -> 10.7 us); beside
-    // a call that keeps all SMs it cost more (causal B4 H16 L4096 d128: 453 -> 461).  Not
+    // a call that keeps all SMs it cost more (100 of them one after another, causal B4 H16 L4096
+    // d128: 453 -> 461).  Not
     // earlier: this block's tensor memory is its own by now.
     sm100::grid_wait();
     if (p.n_items <= static_cast<int>(gridDim.x)) sm100::grid_launch_dependents();
