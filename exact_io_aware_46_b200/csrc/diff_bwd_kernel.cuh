@@ -45,11 +45,11 @@
 // at a time 2715 us; dQ by reductions 2392; halves in turn 2031; fewer waits and no
 // divisions 1869; P_2 and dS in one go 1672; dK_1 by TS 1637; set-up overlapped with the
 // kernel before 1601; P_1 kept as scaled fp16 1638 (for its precision).  What bounds it now is
-// not established.  A 128-row tile takes ~6300 cycles.  Its products read 416 KB of operands from
-// shared memory and copies, dS and statistics' broadcasts pass another 190 KB, ~4850 cycles at
-// 128 bytes a cycle; but with a third of those cycles' worth of statistics' reads left out (timing
-// only) it ran 1.6 % faster, so that is not the limit alone.  The tensor pipe is 51 % active and
-// 68 % busy on its issue side, the special-function unit 35 %, issue 43 %.
+// not established.  A 128-row tile takes ~6300 cycles.  Counted in cycles of shared memory its
+// products' operands take 3250 (416 KB), the copies in 512, dS 512 and the statistics' reads
+// (a wavefront a value and warp) 2048, as many in all; but without those reads (timing only) it
+// ran 1.6 % faster, so they do not simply add up.  The tensor pipe is 51 % active and 68 % busy
+// on its issue side, the special-function unit 35 %, issue 43 %.
 //
 // dlam needs more of P_2 than bf16 gives: its terms P_2 dP have both signs, and
 // the roundings of P_2 (2^-9 relative on average) do not shrink with the sum.
